@@ -22,12 +22,15 @@ OMNI_TOKEN_ORDER = 4
 OMNI_TOPK_BLOCKWISE = 8
 OMNI_EXPERT_DENSE = 16
 OMNI_EXPERT_SPARSE = 32
+OMNI_X_F32 = 64
+OMNI_DX_ACCUMULATE = 128
 
 STATUS = {0: "OMNI_OK", -1: "OMNI_ERR_INVALID_ARG", -2: "OMNI_ERR_UNSUPPORTED",
           -3: "OMNI_ERR_WORKSPACE", -4: "OMNI_ERR_CUDA", -5: "OMNI_ERR_DEVICE"}
 
 # exported symbols and their ctypes signatures (kept in step with include/omni.h)
 _P, _I, _U, _Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_uint, ctypes.c_size_t
+_F = ctypes.c_float
 SIGNATURES = {
     "omni_version": ([], _I),
     "omni_status_string": ([_I], ctypes.c_char_p),
@@ -49,6 +52,20 @@ SIGNATURES = {
                          _U, _P, _Z, _P], _I),
     "omni_shared_mlp_workspace_size": ([_I, _I, _I], _Z),
     "omni_shared_mlp_fwd": ([_P, _P, _P, _P, _I, _I, _I, _P, _U, _P, _Z, _P], _I),
+    "omni_expert_counts": ([_P, _P, _I, _I, _I, _P, _P, _P, _Z, _P], _I),
+    "omni_balance_fwd_workspace_size": ([_I, _I, _I], _Z),
+    "omni_balance_fwd": ([_P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _Z, _P], _I),
+    "omni_balance_bwd_workspace_size": ([_I, _I, _I, _I], _Z),
+    "omni_balance_bwd": ([_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _P, _P, _P,
+                          _U, _P, _Z, _P], _I),
+    "omni_layer_norm_fwd": ([_P, _P, _P, _I, _I, _F, _P, _P, _P, _P, _P, _U, _P], _I),
+    "omni_layer_norm_bwd_workspace_size": ([_I, _I], _Z),
+    "omni_layer_norm_bwd": ([_P, _P, _P, _P, _P, _P, _P, _I, _I, _P, _P, _P, _U, _P, _Z, _P], _I),
+    "omni_act_pack": ([_P, _I, _I, _P, _P, _U, _P], _I),
+    "omni_act_unpack": ([_P, _P, _P, _P, _I, _I, _P, _P], _I),
+    "omni_routed_bwd_ckpt_workspace_size": ([_I, _I, _I, _I, _I], _Z),
+    "omni_routed_bwd_ckpt": ([_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P,
+                              _P, _P, _P, _P, _U, _P, _Z, _P], _I),
     "omni_get_device_status": ([_P, _Z, _P, ctypes.POINTER(ctypes.c_int)], _I),
     "omni_selftest_wait_timeout": ([_P, _Z, _I, _P], _I),
     "omni_grouped_expert_fwd_noalloc": ([_P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P,
@@ -215,6 +232,79 @@ def omni_shared_mlp_fwd(x, W_g, W_u, W_d, L, d, F, y, flags, ws, stream=None):
     rc = load().omni_shared_mlp_fwd(_ptr(x), _ptr(W_g), _ptr(W_u), _ptr(W_d), L, d, F, _ptr(y),
                                     flags, _ptr(ws), ws.numel(), _stream(stream))
     _check("omni_shared_mlp_fwd", rc)
+
+
+def omni_expert_counts(idx, mask, L, K, N, counts, n_tokens, ws, stream=None):
+    rc = load().omni_expert_counts(_ptr(idx), _ptr(mask), L, K, N, _ptr(counts), _ptr(n_tokens),
+                                   _ptr(ws), ws.numel(), _stream(stream))
+    _check("omni_expert_counts", rc)
+
+
+def omni_balance_fwd_workspace_size(L, N_r, N_c) -> int:
+    return int(load().omni_balance_fwd_workspace_size(L, N_r, N_c))
+
+
+def omni_balance_fwd(p_r, p_c, counts, n_tokens, mask, L, N_r, N_c, K, loss, token_loss, ws,
+                     stream=None):
+    rc = load().omni_balance_fwd(_ptr(p_r), _ptr(p_c), _ptr(counts), _ptr(n_tokens), _ptr(mask), L,
+                                 N_r, N_c, K, _ptr(loss), _ptr(token_loss), _ptr(ws), ws.numel(),
+                                 _stream(stream))
+    _check("omni_balance_fwd", rc)
+
+
+def omni_balance_bwd_workspace_size(L, d, N_r, N_c) -> int:
+    return int(load().omni_balance_bwd_workspace_size(L, d, N_r, N_c))
+
+
+def omni_balance_bwd(x, W_r, W_c, p_r, p_c, counts, n_tokens, mask, token_loss, L, d, N_r, N_c, K,
+                     dloss, dx, dW_r, dW_c, flags, ws, stream=None):
+    rc = load().omni_balance_bwd(_ptr(x), _ptr(W_r), _ptr(W_c), _ptr(p_r), _ptr(p_c), _ptr(counts),
+                                 _ptr(n_tokens), _ptr(mask), _ptr(token_loss), L, d, N_r, N_c, K,
+                                 dloss, _ptr(dx), _ptr(dW_r), _ptr(dW_c), flags, _ptr(ws),
+                                 ws.numel(), _stream(stream))
+    _check("omni_balance_bwd", rc)
+
+
+def omni_layer_norm_fwd(x, w, b, L, d, eps, y, mean, rstd, q, scale, flags, stream=None):
+    rc = load().omni_layer_norm_fwd(_ptr(x), _ptr(w), _ptr(b), L, d, eps, _ptr(y), _ptr(mean),
+                                    _ptr(rstd), _ptr(q), _ptr(scale), flags, _stream(stream))
+    _check("omni_layer_norm_fwd", rc)
+
+
+def omni_layer_norm_bwd_workspace_size(L, d) -> int:
+    return int(load().omni_layer_norm_bwd_workspace_size(L, d))
+
+
+def omni_layer_norm_bwd(x, mean, rstd, q, scale, w, dy, L, d, dx, dw, db, flags, ws, stream=None):
+    rc = load().omni_layer_norm_bwd(_ptr(x), _ptr(mean), _ptr(rstd), _ptr(q), _ptr(scale), _ptr(w),
+                                    _ptr(dy), L, d, _ptr(dx), _ptr(dw), _ptr(db), flags, _ptr(ws),
+                                    ws.numel(), _stream(stream))
+    _check("omni_layer_norm_bwd", rc)
+
+
+def omni_act_pack(x, L, d, q, scale, flags, stream=None):
+    rc = load().omni_act_pack(_ptr(x), L, d, _ptr(q), _ptr(scale), flags, _stream(stream))
+    _check("omni_act_pack", rc)
+
+
+def omni_act_unpack(q, scale, w, b, L, d, y, stream=None):
+    rc = load().omni_act_unpack(_ptr(q), _ptr(scale), _ptr(w), _ptr(b), L, d, _ptr(y),
+                                _stream(stream))
+    _check("omni_act_unpack", rc)
+
+
+def omni_routed_bwd_ckpt_workspace_size(L, d, N_r, N_c, K) -> int:
+    return int(load().omni_routed_bwd_ckpt_workspace_size(L, d, N_r, N_c, K))
+
+
+def omni_routed_bwd_ckpt(q, scale, w, b, W, V, W_r, W_c, L, d, N_r, N_c, K, idx, gate, dy, dx, dW,
+                         dV, dW_r, dW_c, flags, ws, stream=None):
+    rc = load().omni_routed_bwd_ckpt(_ptr(q), _ptr(scale), _ptr(w), _ptr(b), _ptr(W), _ptr(V),
+                                     _ptr(W_r), _ptr(W_c), L, d, N_r, N_c, K, _ptr(idx),
+                                     _ptr(gate), _ptr(dy), _ptr(dx), _ptr(dW), _ptr(dV),
+                                     _ptr(dW_r), _ptr(dW_c), flags, _ptr(ws), ws.numel(),
+                                     _stream(stream))
+    _check("omni_routed_bwd_ckpt", rc)
 
 
 def omni_get_device_status(ws, stream=None) -> int:

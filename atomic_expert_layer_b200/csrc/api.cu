@@ -195,6 +195,35 @@ int reset_workspace(void *ws, const WsLayout &lay, cudaStream_t st) {
     return cuda_rc(cudaMemsetAsync(ws, 0, lay.zero_end, st));
 }
 
+// Grid sizes of the balance calls (K only scales them).
+int check_grid(int L, int N_r, int N_c, int K) {
+    if (L <= 0 || N_r <= 0 || N_c <= 0 || K <= 0) return OMNI_ERR_INVALID_ARG;
+    if (N_r > OMNI_MAX_AXIS || N_c > OMNI_MAX_AXIS) return OMNI_ERR_UNSUPPORTED;
+    return OMNI_OK;
+}
+
+int check_ckpt(int L, int d) {
+    if (L <= 0 || d <= 0) return OMNI_ERR_INVALID_ARG;
+    return d % 32 != 0 ? OMNI_ERR_UNSUPPORTED : OMNI_OK;
+}
+
+int check_norm(int L, int d, bool ckpt) {
+    if (L <= 0 || d <= 0) return OMNI_ERR_INVALID_ARG;
+    if (d % (ckpt ? 32 : 8) != 0 || d > OMNI_MAX_NORM_D) return OMNI_ERR_UNSUPPORTED;
+    return OMNI_OK;
+}
+
+int check_plain_ws(void *ws, size_t ws_bytes, size_t need) {
+    if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return OMNI_ERR_INVALID_ARG;
+    return ws_bytes < need ? OMNI_ERR_WORKSPACE : OMNI_OK;
+}
+
+// Clears a workspace's header: the status word and the counters in it.
+int clear_header(void *ws, cudaStream_t st) {
+    first_launch_in_call();
+    return cuda_rc(cudaMemsetAsync(ws, 0, sizeof(WsHeader), st));
+}
+
 int router_topk_impl(const uint16_t *x, const uint16_t *W_r, const uint16_t *W_c,
                      const Sizes &sz, float *p_r, float *p_c, int32_t *idx, float *score,
                      float *gate, unsigned flags, void *ws, const WsLayout &lay,
@@ -557,6 +586,169 @@ int omni_shared_mlp_fwd(const omni_bf16 *x, const omni_bf16 *W_g, const omni_bf1
     uint16_t *h = ws_at<uint16_t>(ws, sizeof(WsHeader));
     return cuda_rc(launch_shared_mlp(x, W_g, W_u, W_d, L, d, F, h, y,
                                      (flags & OMNI_Y_ACCUMULATE) != 0, ws_at<int>(ws, 0), st));
+}
+
+int omni_expert_counts(const int32_t *idx, const uint8_t *mask, int L, int K, int N,
+                       int32_t *counts, int32_t *n_tokens, void *ws, size_t ws_bytes,
+                       omni_stream_t stream) {
+    if (!idx || !counts || !n_tokens || !ws || L <= 0 || K <= 0 || N <= 0)
+        return OMNI_ERR_INVALID_ARG;
+    if ((int64_t)L * K > INT_MAX) return OMNI_ERR_UNSUPPORTED;
+    if (!aligned4(idx) || !aligned4(counts) || !aligned4(n_tokens)) return OMNI_ERR_INVALID_ARG;
+    int rc = check_plain_ws(ws, ws_bytes, sizeof(WsHeader));
+    if (rc) return rc;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if ((rc = clear_header(ws, st))) return rc;
+    return cuda_rc(launch_counts(idx, mask, (int64_t)L * K, K, N, counts, n_tokens,
+                                 ws_at<int>(ws, 0), st));
+}
+
+size_t omni_balance_fwd_workspace_size(int L, int N_r, int N_c) {
+    if (check_grid(L, N_r, N_c, 1) != OMNI_OK) return 0;
+    return balance_ws(L, 0, N_r, N_c, false).total;
+}
+
+size_t omni_balance_bwd_workspace_size(int L, int d, int N_r, int N_c) {
+    if (check_grid(L, N_r, N_c, 1) != OMNI_OK || d <= 0 || d % 8 != 0) return 0;
+    return balance_ws(L, d, N_r, N_c, true).total;
+}
+
+int omni_balance_fwd(const float *p_r, const float *p_c, const int32_t *counts,
+                     const int32_t *n_tokens, const uint8_t *mask, int L, int N_r, int N_c, int K,
+                     float *loss, float *token_loss, void *ws, size_t ws_bytes,
+                     omni_stream_t stream) {
+    int rc = check_grid(L, N_r, N_c, K);
+    if (rc) return rc;
+    if (!p_r || !p_c || !counts || !n_tokens || !loss || !token_loss || !ws)
+        return OMNI_ERR_INVALID_ARG;
+    if (!aligned4(p_r) || !aligned4(p_c) || !aligned4(counts) || !aligned4(n_tokens) ||
+        !aligned4(loss) || !aligned4(token_loss))
+        return OMNI_ERR_INVALID_ARG;
+    if ((rc = check_plain_ws(ws, ws_bytes, omni_balance_fwd_workspace_size(L, N_r, N_c)))) return rc;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if ((rc = clear_header(ws, st))) return rc;
+    return cuda_rc(launch_balance_fwd(p_r, p_c, counts, n_tokens, mask, L, N_r, N_c, K, loss,
+                                      token_loss, ws, st));
+}
+
+int omni_balance_bwd(const omni_bf16 *x, const omni_bf16 *W_r, const omni_bf16 *W_c,
+                     const float *p_r, const float *p_c, const int32_t *counts,
+                     const int32_t *n_tokens, const uint8_t *mask, const float *token_loss, int L,
+                     int d, int N_r, int N_c, int K, float dloss, float *dx, float *dW_r,
+                     float *dW_c, unsigned flags, void *ws, size_t ws_bytes,
+                     omni_stream_t stream) {
+    int rc = check_grid(L, N_r, N_c, K);
+    if (rc) return rc;
+    if (d <= 0 || (flags & ~OMNI_DX_ACCUMULATE) != 0) return OMNI_ERR_INVALID_ARG;
+    if (!x || !W_r || !W_c || !p_r || !p_c || !counts || !n_tokens || !token_loss || !dx ||
+        !dW_r || !dW_c || !ws)
+        return OMNI_ERR_INVALID_ARG;
+    if (d % 8 != 0) return OMNI_ERR_UNSUPPORTED;
+    if (!aligned16(x) || !aligned16(W_r) || !aligned16(W_c) || !aligned16(dx) ||
+        !aligned16(dW_r) || !aligned16(dW_c) || !aligned4(p_r) || !aligned4(p_c) ||
+        !aligned4(counts) || !aligned4(n_tokens) || !aligned4(token_loss))
+        return OMNI_ERR_INVALID_ARG;
+    if ((rc = check_plain_ws(ws, ws_bytes, omni_balance_bwd_workspace_size(L, d, N_r, N_c))))
+        return rc;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if ((rc = clear_header(ws, st))) return rc;
+    return cuda_rc(launch_balance_bwd(x, W_r, W_c, p_r, p_c, counts, n_tokens, mask, token_loss, L,
+                                      d, N_r, N_c, K, dloss, dx, (flags & OMNI_DX_ACCUMULATE) != 0,
+                                      dW_r, dW_c, ws, st));
+}
+
+int omni_layer_norm_fwd(const void *x, const omni_bf16 *w, const omni_bf16 *b, int L, int d,
+                        float eps, omni_bf16 *y, float *mean, float *rstd, uint8_t *q,
+                        uint8_t *scale, unsigned flags, omni_stream_t stream) {
+    int rc = check_norm(L, d, q != nullptr);
+    if (rc) return rc;
+    if ((flags & ~OMNI_X_F32) != 0 || !(eps >= 0.f) || !x || !w || !y || !q != !scale)
+        return OMNI_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(w) || !aligned16(b) || !aligned16(y) || !aligned16(q) ||
+        !aligned4(mean) || !aligned4(rstd))
+        return OMNI_ERR_INVALID_ARG;
+    first_launch_in_call();
+    return cuda_rc(launch_norm_fwd(x, (flags & OMNI_X_F32) != 0, w, b, L, d, eps, y, mean, rstd, q,
+                                   scale, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t omni_layer_norm_bwd_workspace_size(int L, int d) {
+    if (check_norm(L, d, false) != OMNI_OK) return 0;
+    return sizeof(WsHeader) + align256((size_t)norm_bwd_parts(L, d) * 2 * (size_t)d * sizeof(float));
+}
+
+int omni_layer_norm_bwd(const void *x, const float *mean, const float *rstd, const uint8_t *q,
+                        const uint8_t *scale, const omni_bf16 *w, const float *dy, int L, int d,
+                        float *dx, float *dw, float *db, unsigned flags, void *ws, size_t ws_bytes,
+                        omni_stream_t stream) {
+    int rc = check_norm(L, d, q != nullptr);
+    if (rc) return rc;
+    if ((flags & ~(OMNI_X_F32 | OMNI_DX_ACCUMULATE)) != 0) return OMNI_ERR_INVALID_ARG;
+    if (!rstd || !w || !dy || !dx || !dw || !ws || !q != !scale || (!q && (!x || !mean)))
+        return OMNI_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(q) || !aligned16(w) || !aligned16(dy) || !aligned16(dx) ||
+        !aligned16(dw) || !aligned16(db) || !aligned4(mean) || !aligned4(rstd))
+        return OMNI_ERR_INVALID_ARG;
+    if ((rc = check_plain_ws(ws, ws_bytes, omni_layer_norm_bwd_workspace_size(L, d)))) return rc;
+    first_launch_in_call();
+    return cuda_rc(launch_norm_bwd(x, (flags & OMNI_X_F32) != 0, mean, rstd, q, scale, w, dy, L, d,
+                                   dx, (flags & OMNI_DX_ACCUMULATE) != 0, dw, db,
+                                   ws_at<float>(ws, sizeof(WsHeader)),
+                                   reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int omni_act_pack(const void *x, int L, int d, uint8_t *q, uint8_t *scale, unsigned flags,
+                  omni_stream_t stream) {
+    const int rc = check_ckpt(L, d);
+    if (rc) return rc;
+    if ((flags & ~OMNI_X_F32) != 0 || !x || !q || !scale || !aligned16(x) || !aligned16(q))
+        return OMNI_ERR_INVALID_ARG;
+    first_launch_in_call();
+    return cuda_rc(launch_ckpt_pack(x, (flags & OMNI_X_F32) != 0, L, d, q, scale,
+                                    reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int omni_act_unpack(const uint8_t *q, const uint8_t *scale, const omni_bf16 *w,
+                    const omni_bf16 *b, int L, int d, omni_bf16 *y, omni_stream_t stream) {
+    const int rc = check_ckpt(L, d);
+    if (rc) return rc;
+    if (!q || !scale || !y || (b && !w) || !aligned16(q) || !aligned16(w) || !aligned16(b) ||
+        !aligned16(y))
+        return OMNI_ERR_INVALID_ARG;
+    first_launch_in_call();
+    return cuda_rc(launch_ckpt_unpack(q, scale, w, b, L, d, y,
+                                      reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t omni_routed_bwd_ckpt_workspace_size(int L, int d, int N_r, int N_c, int K) {
+    const size_t bwd = omni_routed_bwd_workspace_size(L, d, N_r, N_c, K);
+    return bwd == 0 ? 0 : bwd + align256(2 * (size_t)L * (size_t)d);
+}
+
+int omni_routed_bwd_ckpt(const uint8_t *q, const uint8_t *scale, const omni_bf16 *w,
+                         const omni_bf16 *b, const omni_bf16 *W, const omni_bf16 *V,
+                         const omni_bf16 *W_r, const omni_bf16 *W_c, int L, int d, int N_r,
+                         int N_c, int K, const int32_t *idx, const float *gate, const float *dy,
+                         float *dx, float *dW, float *dV, float *dW_r, float *dW_c, unsigned flags,
+                         void *ws, size_t ws_bytes, omni_stream_t stream) {
+    Sizes sz;
+    int rc = check_common(L, d, N_r, N_c, K, 1, true, &sz);
+    if (rc) return rc;
+    // everything omni_routed_bwd checks, before the restoring launch
+    if (!W || !V || !W_r || !W_c || !idx || !gate || !dy || !dx || !dW || !dV || !dW_r || !dW_c ||
+        !ws || flags != 0)
+        return OMNI_ERR_INVALID_ARG;
+    if (d % 256 != 0 || d > OMNI_MAX_D) return OMNI_ERR_UNSUPPORTED;
+    if (!aligned16(W) || !aligned16(V) || !aligned16(W_r) || !aligned16(W_c) || !aligned16(dy) ||
+        !aligned16(dx) || !aligned16(dW) || !aligned16(dV) || !aligned16(dW_r) || !aligned16(dW_c))
+        return OMNI_ERR_INVALID_ARG;
+    if ((rc = check_plain_ws(ws, ws_bytes, omni_routed_bwd_ckpt_workspace_size(L, d, N_r, N_c, K))))
+        return rc;
+    const size_t bwd = omni_routed_bwd_workspace_size(L, d, N_r, N_c, K);
+    uint16_t *x = ws_at<uint16_t>(ws, bwd);
+    if ((rc = omni_act_unpack(q, scale, w, b, L, d, x, stream))) return rc;
+    return omni_routed_bwd(x, W, V, W_r, W_c, L, d, N_r, N_c, K, idx, gate, dy, dx, dW, dV, dW_r,
+                           dW_c, flags, ws, bwd, stream);
 }
 
 int omni_selftest_wait_timeout(void *ws, size_t ws_bytes, int limit_ms, omni_stream_t stream) {

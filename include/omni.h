@@ -72,6 +72,8 @@ typedef enum {
 #define OMNI_TOPK_BLOCKWISE     8u  /* omni_router_topk: the pages' blockwise grid top-K (below)           */
 #define OMNI_EXPERT_DENSE      16u  /* expert stage: always try the tensor-core tiles for dense experts   */
 #define OMNI_EXPERT_SPARSE     32u  /* expert stage: every task on the task-by-task path (no tiles)       */
+#define OMNI_X_F32             64u  /* layer norm, checkpoints: x is fp32 (a residual stream), not bf16   */
+#define OMNI_DX_ACCUMULATE    128u  /* layer norm and balance backward: dx += gradient instead of dx =    */
 
 /* Device status codes written into the workspace status word. */
 #define OMNI_DEV_OK              0
@@ -84,6 +86,7 @@ typedef enum {
 #define OMNI_MAX_K      512         /* K                                          */
 #define OMNI_MAX_B      1024        /* B                                          */
 #define OMNI_MAX_D      2048        /* d for the expert stage; d % 256 == 0 there */
+#define OMNI_MAX_NORM_D 8192        /* d for the layer norm                       */
 
 /* Library version, for the binding's sanity check. */
 int omni_version(void);
@@ -317,6 +320,140 @@ size_t omni_shared_mlp_workspace_size(int L, int d, int F);
 int omni_shared_mlp_fwd(const omni_bf16 *x, const omni_bf16 *W_g, const omni_bf16 *W_u,
                         const omni_bf16 *W_d, int L, int d, int F, float *y, unsigned flags,
                         void *ws, size_t ws_bytes, omni_stream_t stream);
+
+/*
+ * Tasks per expert, for the balance loss and for monitoring.  The pages have
+ * no counterpart.
+ *   counts[e] = number of (t, k) with idx[t, k] = e and mask[t] != 0   [N] int32
+ *   n_tokens  = number of tokens with mask[t] != 0                     [1] int32
+ * idx [L, K] int32 (omni_router_topk's); mask [L] bytes, NULL = every token
+ * counts (padding tokens have mask 0; their ids are not read).  Both outputs
+ * are overwritten and do not depend on the order of the atomics.  An id
+ * outside [0, N) sets OMNI_DEV_BAD_EXPERT and is not counted.  ws: at least
+ * 256 bytes.  With several replicas, the counts and n_tokens may be summed
+ * over the replicas before the balance calls.  Limits: L * K and N < 2^31.
+ */
+int omni_expert_counts(const int32_t *idx, const uint8_t *mask, int L, int K, int N,
+                       int32_t *counts, int32_t *n_tokens, void *ws, size_t ws_bytes,
+                       omni_stream_t stream);
+
+/*
+ * Balance loss of the router over its N = N_r * N_c experts, and its
+ * gradients.  The pages give none; this is the product of the experts' shares
+ * of the tasks and of the probability,
+ *   loss = N sum_e f_e P_e,   f_e = counts[e] / (K n),
+ *   P_e  = mean over the kept tokens of exp(p_r[t, i]) exp(p_c[t, j]), e = (i, j)
+ * (1 for a router that spreads both evenly), with n = n_tokens[0] and the mean
+ * over the tokens of this call with mask[t] != 0 (NULL = all).  The softmax
+ * over the grid is the product of its axes' softmaxes, so the [L, N]
+ * probabilities are never built: U = P_c F^T with F the counts as [N_r, N_c],
+ *   token_loss[t] = sum_i exp(p_r[t, i]) U[t, i]   [L] fp32 output (0 where masked)
+ *   loss [1] fp32 output = N / (K n n_kept) sum_t token_loss[t]
+ * With no token kept (or n = 0) the loss and all gradients are 0.
+ *   p_r [L, N_r], p_c [L, N_c] fp32 log-probabilities (omni_router_topk's;
+ *   -inf is a probability of 0); the rows of masked tokens are not read.
+ *   counts [N], n_tokens [1] int32 of omni_expert_counts (or sums of them over
+ *   replicas; values up to 2^22 are taken exactly, larger ones to 22 bits).
+ * The backward takes the gradient of dloss * loss, the counts held fixed (a
+ * selection has no gradient), through the LogSoftmax to the tokens and the
+ * router's weights:
+ *   ds_r[t, i] = c exp(p_r[t, i]) (U[t, i] - token_loss[t]), c = dloss N / (K n n_kept)
+ *   ds_c[t, j] likewise with V = P_r F
+ *   dx [L, d] fp32    = ds_r W_r + ds_c W_c, or added to dx with OMNI_DX_ACCUMULATE
+ *                       (so that it joins omni_routed_bwd's); masked rows get 0
+ *   dW_r [N_r, d], dW_c [N_c, d] fp32  += ds^T x, accumulated
+ *   x [L, d], W_r, W_c bf16 (the forward's; the rows of masked tokens of x do
+ *   not matter); token_loss is the forward's.
+ * Products run on the tensor cores with fp32 sums: exp(p) enters as two fp16
+ * values (hi + lo, 22 bits; exp(p) must stay below 4), ds as two bf16 values
+ * (16 bits).  Every output element is written by one tile: the results are the
+ * same on every run.
+ * ws: the size functions' bytes, 256-byte aligned.  dx, dW_r, dW_c, x, W_r,
+ * W_c 16-byte aligned.  d % 8 == 0.  Limits: N_r, N_c <= OMNI_MAX_AXIS,
+ * N < 2^31.
+ */
+size_t omni_balance_fwd_workspace_size(int L, int N_r, int N_c);
+int omni_balance_fwd(const float *p_r, const float *p_c, const int32_t *counts,
+                     const int32_t *n_tokens, const uint8_t *mask, int L, int N_r, int N_c, int K,
+                     float *loss, float *token_loss, void *ws, size_t ws_bytes,
+                     omni_stream_t stream);
+size_t omni_balance_bwd_workspace_size(int L, int d, int N_r, int N_c);
+int omni_balance_bwd(const omni_bf16 *x, const omni_bf16 *W_r, const omni_bf16 *W_c,
+                     const float *p_r, const float *p_c, const int32_t *counts,
+                     const int32_t *n_tokens, const uint8_t *mask, const float *token_loss, int L,
+                     int d, int N_r, int N_c, int K, float dloss, float *dx, float *dW_r,
+                     float *dW_c, unsigned flags, void *ws, size_t ws_bytes, omni_stream_t stream);
+
+/*
+ * Layer norm of L rows of d values: the layer's x is the normed residual
+ * stream.  The pages have no counterpart.
+ *   mean = sum x / d,  var = sum (x - mean)^2 / d,  rstd = 1 / sqrt(var + eps)
+ *   xh = (x - mean) rstd,  y = xh w + b
+ *   x [L, d] bf16, or fp32 with OMNI_X_F32;  w [d] bf16;  b [d] bf16 or NULL
+ *   y [L, d] bf16 output;  mean, rstd [L] fp32 outputs, each NULL to skip
+ *   q [L, d], scale [L, d / 32] bytes: optional outputs (both or neither), the
+ *   8-bit checkpoint of xh (omni_act_pack's form); d % 32 == 0 with them.
+ * eps >= 0 (a constant row has xh = 0 with eps > 0).  d % 8 == 0,
+ * d <= OMNI_MAX_NORM_D.  Arrays 16-byte aligned (mean, rstd 4, scale 1).
+ */
+int omni_layer_norm_fwd(const void *x, const omni_bf16 *w, const omni_bf16 *b, int L, int d,
+                        float eps, omni_bf16 *y, float *mean, float *rstd, uint8_t *q,
+                        uint8_t *scale, unsigned flags, omni_stream_t stream);
+
+/*
+ * Its backward.  The rows come from (x, mean) or, where q is not NULL, from
+ * the forward's checkpoint (x and mean are then not read and may be NULL):
+ *   g = dy w,  dx = rstd (g - mean(g) - xh mean(g xh))
+ *   dy [L, d] fp32 (omni_routed_bwd's dx);  rstd [L] fp32 of the forward
+ *   dx [L, d] fp32 output, or added to dx with OMNI_DX_ACCUMULATE; dx may be dy
+ *   (without the flag)
+ *   dw [d], db [d] fp32  accumulated (+=): sum_t dy xh, sum_t dy; db may be NULL
+ * The sums over the rows run in a fixed order: the results are the same on
+ * every run.  ws: omni_layer_norm_bwd_workspace_size(L, d) bytes, 256-byte
+ * aligned.  Limits as for the forward; fp32 arrays 16-byte aligned (mean,
+ * rstd 4).
+ */
+size_t omni_layer_norm_bwd_workspace_size(int L, int d);
+int omni_layer_norm_bwd(const void *x, const float *mean, const float *rstd, const uint8_t *q,
+                        const uint8_t *scale, const omni_bf16 *w, const float *dy, int L, int d,
+                        float *dx, float *dw, float *db, unsigned flags, void *ws, size_t ws_bytes,
+                        omni_stream_t stream);
+
+/*
+ * 8-bit activation checkpoints: what a layer keeps between its forward and its
+ * backward, in about half of bf16's bytes.  The pages have no counterpart.
+ * Blocks of 32 values of a row share one scale byte:
+ *   value = q 2^(scale - 127), q in e4m3 (4 exponent bits, 3 mantissa bits,
+ *   largest 448), the scale the smallest power of two (from 2^-127 on) that
+ *   lets no value of the block pass 448.  Each value is rounded once, to
+ *   nearest even: off by at most 2^-4 of itself, or 2^-10 of the scale near 0.
+ *   Infinities and NaN become NaN and do not move the block's scale.
+ * pack:   x [L, d] bf16 (fp32 with OMNI_X_F32) -> q [L, d], scale [L, d / 32] bytes
+ * unpack: y [L, d] bf16 = value, or value * w + b rounded once (w, b [d] bf16;
+ *         b may be NULL, and w with it): the normed tokens from
+ *         omni_layer_norm_fwd's checkpoint
+ * d % 32 == 0.  x, q, y, w, b 16-byte aligned.
+ */
+int omni_act_pack(const void *x, int L, int d, uint8_t *q, uint8_t *scale, unsigned flags,
+                  omni_stream_t stream);
+int omni_act_unpack(const uint8_t *q, const uint8_t *scale, const omni_bf16 *w,
+                    const omni_bf16 *b, int L, int d, omni_bf16 *y, omni_stream_t stream);
+
+/*
+ * omni_routed_bwd with its tokens taken from a checkpoint:
+ * x = omni_act_unpack(q, scale, w, b), then the same arguments and results
+ * (dx is the gradient with respect to that x).  The experts and the router
+ * see the restored tokens; idx and gate are the forward's.
+ * ws: omni_routed_bwd_ckpt_workspace_size(...) bytes, 256-byte aligned (the
+ * fast path's workspace and the restored tokens, 2 L d bytes).
+ */
+size_t omni_routed_bwd_ckpt_workspace_size(int L, int d, int N_r, int N_c, int K);
+int omni_routed_bwd_ckpt(const uint8_t *q, const uint8_t *scale, const omni_bf16 *w,
+                         const omni_bf16 *b, const omni_bf16 *W, const omni_bf16 *V,
+                         const omni_bf16 *W_r, const omni_bf16 *W_c, int L, int d, int N_r,
+                         int N_c, int K, const int32_t *idx, const float *gate, const float *dy,
+                         float *dx, float *dW, float *dV, float *dW_r, float *dW_c, unsigned flags,
+                         void *ws, size_t ws_bytes, omni_stream_t stream);
 
 /*
  * omni_grouped_expert_fwd without a workspace, for callers that cannot

@@ -1,0 +1,211 @@
+"""The training operators on the host: the references that their GPU tests use,
+against differences and brute force, workspace sizes, and the refusals of the C
+entry points and of the wrappers.  Nothing here reaches a GPU."""
+import ctypes
+
+import pytest
+import torch
+
+import atomic_expert_layer_b200 as omni
+from atomic_expert_layer_b200 import _lib, build
+
+import _train_ref as ref
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return _lib.load()
+
+
+def _p(v):
+    return ctypes.c_void_p(v)
+
+
+FAKE = _p(1 << 20)                       # 16-byte aligned, never dereferenced
+ODD = _p((1 << 20) + 2)
+BIG = 1 << 34
+
+
+# ------------------------------------------------------------- references
+def test_balance_reference_against_differences():
+    """d(dloss * loss) along random directions of x, W_r, W_c, by central
+    differences of the definition over all N experts (64 bits: the step 1e-5
+    leaves 1e-10 of truncation and 1e-11 of rounding, relative to O(1) slopes)."""
+    g = torch.Generator().manual_seed(3)
+    L, d, N_r, N_c, K, dloss = 11, 16, 5, 7, 3, 0.7
+    x, W_r, W_c = (torch.randn(n, d, generator=g, dtype=torch.float64) for n in (L, N_r, N_c))
+    idx = torch.stack([torch.randperm(N_r * N_c, generator=g)[:K] for _ in range(L)]).int()
+    mask = torch.rand(L, generator=g) > 0.3
+    counts, n = ref.counts_ref(idx, N_r * N_c, mask)
+    assert counts.sum() == n * K
+
+    def loss(x, W_r, W_c):
+        return dloss * ref.balance_loss_ref(x @ W_r.T, x @ W_c.T, counts, n, K, mask)
+
+    got = ref.balance_ref(x, W_r, W_c, torch.log_softmax(x @ W_r.T, 1),
+                          torch.log_softmax(x @ W_c.T, 1), counts, n, K, dloss, mask)
+    assert abs(dloss * got["loss"] - loss(x, W_r, W_c)) < 1e-12
+    args = [x, W_r, W_c]
+    for at, name in enumerate(("dx", "dW_r", "dW_c")):
+        for _ in range(4):
+            v = torch.randn(args[at].shape, generator=g, dtype=torch.float64)
+            up, dn = list(args), list(args)
+            up[at], dn[at] = args[at] + 1e-5 * v, args[at] - 1e-5 * v
+            num = (loss(*up) - loss(*dn)) / 2e-5
+            assert abs(num - (got[name] * v).sum()) < 1e-7 * max(1.0, abs(num))
+
+
+def test_balance_reference_is_one_when_even():
+    # every expert taken once, uniform probabilities: N * N * (1/N)(1/N) = 1
+    N_r, N_c = 4, 6
+    idx = torch.arange(24).reshape(12, 2).int()
+    counts, n = ref.counts_ref(idx, 24)
+    z = torch.zeros(12, N_r, dtype=torch.float64), torch.zeros(12, N_c, dtype=torch.float64)
+    assert abs(ref.balance_loss_ref(*z, counts, n, 2) - 1) < 1e-12
+
+
+def test_norm_reference_against_differences():
+    g = torch.Generator().manual_seed(5)
+    L, d, eps = 4, 24, 1e-5
+    x, dy = (torch.randn(L, d, generator=g, dtype=torch.float64) for _ in range(2))
+    w, b = (torch.randn(d, generator=g, dtype=torch.float64) for _ in range(2))
+    _, _, rstd, xh = ref.norm_ref(x, w, b, eps)
+    got = ref.norm_bwd_ref(dy, w, rstd, xh)
+    f = lambda x, w, b: (dy * ref.norm_ref(x, w, b, eps)[0]).sum()  # noqa: E731
+    for at, name in enumerate(("dx", "dw", "db")):
+        args = [x, w, b]
+        v = torch.randn(args[at].shape, generator=g, dtype=torch.float64)
+        up, dn = list(args), list(args)
+        up[at], dn[at] = args[at] + 1e-5 * v, args[at] - 1e-5 * v
+        num = (f(*up) - f(*dn)) / 2e-5
+        assert abs(num - (got[name] * v).sum()) < 1e-7 * max(1.0, abs(num))
+
+
+def test_pack_reference_by_hand():
+    x = torch.zeros(1, 64)
+    x[0, 0], x[0, 1], x[0, 2], x[0, 3] = 448.0, -1.0, 449.0, 0.0
+    q, code, _ = ref.pack_ref(x)
+    # 449 > 448: scale 2, so -1 is -0.5 and 449 / 2 = 224.5 rounds to 224
+    assert code[0, 0] == 128 and code[0, 1] == 0
+    v = ref.unpack_ref(q, code)
+    assert v[0, :4].tolist() == [448.0, -1.0, 448.0, 0.0]
+    x[0, 2] = 0
+    q, code, _ = ref.pack_ref(x)
+    assert code[0, 0] == 127 and ref.unpack_ref(q, code)[0, 0] == 448.0
+
+
+# ------------------------------------------------------- sizes and refusals
+def test_workspace_sizes(lib):
+    assert omni.omni_balance_fwd_workspace_size(0, 8, 8) == 0
+    assert omni.omni_balance_fwd_workspace_size(8, 8193, 8) == 0
+    assert omni.omni_balance_bwd_workspace_size(8, 12, 8, 8) == 0           # d % 8
+    L, d, N_r, N_c = 100, 64, 70, 60
+    pr, pc = 128, 64
+    up = lambda v: -(-v // 256) * 256                                       # noqa: E731
+    fwd = 256 + 2 * up(2 * L * pc) + 2 * up(2 * N_r * pc) + up(4 * 2 * L) + up(8)
+    assert omni.omni_balance_fwd_workspace_size(L, N_r, N_c) == fwd
+    bwd = 256 + 4 * up(2 * L * (pr + pc)) + 2 * up(2 * N_r * pc) + 2 * up(2 * N_c * pr) + up(2 * L * d)
+    assert omni.omni_balance_bwd_workspace_size(L, d, N_r, N_c) == bwd
+    assert omni.omni_layer_norm_bwd_workspace_size(5, 12) == 0
+    assert omni.omni_layer_norm_bwd_workspace_size(5, 8200) == 0
+    assert omni.omni_layer_norm_bwd_workspace_size(5, 1000) % 256 == 0
+    b = omni.omni_routed_bwd_workspace_size(7, 256, 8, 8, 4)
+    assert omni.omni_routed_bwd_ckpt_workspace_size(7, 256, 8, 8, 4) == b + up(2 * 7 * 256)
+    assert omni.omni_routed_bwd_ckpt_workspace_size(7, 256, 8, 8, 0) == 0
+
+
+def _try_all_pointers(fn, args, pointers, optional=()):
+    """Each required pointer as NULL is refused (OMNI_ERR_INVALID_ARG)."""
+    for i in pointers:
+        if i in optional:
+            continue
+        bad = list(args)
+        bad[i] = None
+        assert fn(*bad) == -1, i
+
+
+def test_expert_counts_refusals(lib):
+    ok = [FAKE, None, 4, 2, 16, FAKE, FAKE, FAKE, 256, None]
+    _try_all_pointers(lib.omni_expert_counts, ok, (0, 5, 6, 7))
+    for at, v, rc in ((2, 0, -1), (3, 0, -1), (4, 0, -1), (8, 255, -3), (7, ODD, -1), (0, ODD, -1),
+                      (2, 1 << 30, -2)):
+        bad = list(ok)
+        bad[at] = v
+        if at == 2 and rc == -2:
+            bad[3] = 2
+        assert lib.omni_expert_counts(*bad) == rc, (at, v)
+
+
+def test_balance_refusals(lib):
+    ok = [FAKE, FAKE, FAKE, FAKE, None, 4, 8, 8, 2, FAKE, FAKE, FAKE, BIG, None]
+    _try_all_pointers(lib.omni_balance_fwd, ok, (0, 1, 2, 3, 9, 10, 11))
+    for at, v, rc in ((5, 0, -1), (6, 0, -1), (7, -1, -1), (8, 0, -1), (6, 8193, -2), (7, 8193, -2),
+                      (12, 1000, -3), (0, ODD, -1), (11, _p((1 << 20) + 16), -1)):
+        bad = list(ok)
+        bad[at] = v
+        assert lib.omni_balance_fwd(*bad) == rc, (at, v)
+    ok = [FAKE] * 7 + [None, FAKE, 4, 64, 8, 8, 2, 1.0, FAKE, FAKE, FAKE, 0, FAKE, BIG, None]
+    _try_all_pointers(lib.omni_balance_bwd, ok, (0, 1, 2, 3, 4, 5, 6, 8, 15, 16, 17, 19))
+    for at, v, rc in ((9, 0, -1), (10, 0, -1), (10, 12, -2), (11, 9000, -2), (13, 0, -1), (18, 1, -1),
+                      (20, 1000, -3), (0, ODD, -1), (15, _p((1 << 20) + 4), -1), (3, ODD, -1)):
+        bad = list(ok)
+        bad[at] = v
+        assert lib.omni_balance_bwd(*bad) == rc, (at, v)
+
+
+def test_layer_norm_refusals(lib):
+    ok = [FAKE, FAKE, None, 4, 64, 1e-5, FAKE, None, None, None, None, 0, None]
+    _try_all_pointers(lib.omni_layer_norm_fwd, ok, (0, 1, 6))
+    for at, v, rc in ((3, 0, -1), (4, 0, -1), (4, 12, -2), (4, 8200, -2), (5, -1.0, -1),
+                      (5, float("nan"), -1), (9, FAKE, -1), (10, FAKE, -1), (11, 1, -1),
+                      (11, 128, -1), (0, ODD, -1), (2, ODD, -1), (6, ODD, -1), (7, ODD, -1)):
+        bad = list(ok)
+        bad[at] = v
+        assert lib.omni_layer_norm_fwd(*bad) == rc, (at, v)
+    # a checkpoint needs whole blocks of 32
+    assert lib.omni_layer_norm_fwd(FAKE, FAKE, None, 4, 40, 1e-5, FAKE, None, None, FAKE, FAKE, 0,
+                                   None) == -2
+    ok = [FAKE, FAKE, FAKE, None, None, FAKE, FAKE, 4, 64, FAKE, FAKE, None, 0, FAKE, BIG, None]
+    _try_all_pointers(lib.omni_layer_norm_bwd, ok, (0, 1, 2, 5, 6, 9, 10, 13))
+    for at, v, rc in ((7, 0, -1), (8, 12, -2), (3, FAKE, -1), (4, FAKE, -1), (12, 2, -1), (14, 100, -3),
+                      (6, ODD, -1), (13, _p((1 << 20) + 8), -1), (11, ODD, -1)):
+        bad = list(ok)
+        bad[at] = v
+        assert lib.omni_layer_norm_bwd(*bad) == rc, (at, v)
+
+
+def test_checkpoint_refusals(lib):
+    ok = [FAKE, 4, 64, FAKE, FAKE, 0, None]
+    _try_all_pointers(lib.omni_act_pack, ok, (0, 3, 4))
+    for at, v, rc in ((1, 0, -1), (2, 40, -2), (5, 2, -1), (0, ODD, -1), (3, ODD, -1)):
+        bad = list(ok)
+        bad[at] = v
+        assert lib.omni_act_pack(*bad) == rc, (at, v)
+    ok = [FAKE, FAKE, None, None, 4, 64, FAKE, None]
+    _try_all_pointers(lib.omni_act_unpack, ok, (0, 1, 6))
+    for at, v, rc in ((4, 0, -1), (5, 48, -2), (3, FAKE, -1), (6, ODD, -1), (2, ODD, -1)):
+        bad = list(ok)
+        bad[at] = v
+        assert lib.omni_act_unpack(*bad) == rc, (at, v)
+    ok = [FAKE, FAKE, None, None, FAKE, FAKE, FAKE, FAKE, 4, 256, 8, 8, 2] + [FAKE] * 8 + [0, FAKE, BIG, None]
+    _try_all_pointers(lib.omni_routed_bwd_ckpt, ok, (0, 1, 4, 5, 6, 7, *range(13, 21), 22))
+    for at, v, rc in ((8, 0, -1), (9, 264, -2), (12, 65, -1), (21, 1, -1), (23, 256, -3), (3, FAKE, -1),
+                      (16, ODD, -1)):
+        bad = list(ok)
+        bad[at] = v
+        assert lib.omni_routed_bwd_ckpt(*bad) == rc, (at, v)
+
+
+def test_wrappers_refuse_cpu_tensors(lib):
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    w = torch.zeros(64, dtype=torch.bfloat16)
+    p = torch.zeros(4, 8)
+    i = torch.zeros(4, 2, dtype=torch.int32)
+    for call in (lambda: omni.layer_norm_fwd(x, w), lambda: omni.act_pack(x),
+                 lambda: omni.act_unpack(x.view(torch.uint8), w.view(torch.uint8)),
+                 lambda: omni.expert_counts(i, 16),
+                 lambda: omni.balance_fwd(p, p, torch.zeros(64, dtype=torch.int32), i, 2),
+                 lambda: omni.layer_norm_bwd(p, w, p)):
+        with pytest.raises(ValueError):
+            call()
