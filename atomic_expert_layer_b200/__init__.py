@@ -20,7 +20,7 @@ import torch
 
 from ._lib import (OMNI_ROUTER_LOGPROBS_IN, OMNI_TOKEN_ORDER, OMNI_TOPK_BLOCKWISE,  # noqa: F401
                    OMNI_Y_ACCUMULATE, OMNI_EXPERT_DENSE, OMNI_EXPERT_SPARSE,
-                   OMNI_X_F32, OMNI_DX_ACCUMULATE,
+                   OMNI_X_F32, OMNI_DX_ACCUMULATE, OMNI_DW_OVERWRITE, _check,
                    omni_act_pack, omni_act_unpack, omni_balance_bwd,
                    omni_balance_bwd_workspace_size, omni_balance_fwd,
                    omni_balance_fwd_workspace_size, omni_expert_counts, omni_layer_norm_bwd,
@@ -48,7 +48,7 @@ __all__ = [
     "router_topk", "schedule", "grouped_expert_fwd", "routed_fwd", "omni_routed_bwd", "routed_bwd",
     "omni_routed_bwd_workspace_size",
     "omni_shared_mlp_workspace_size", "omni_shared_mlp_fwd", "shared_mlp_fwd", "layer_fwd",
-    "OMNI_X_F32", "OMNI_DX_ACCUMULATE", "omni_expert_counts", "omni_balance_fwd_workspace_size",
+    "OMNI_X_F32", "OMNI_DX_ACCUMULATE", "OMNI_DW_OVERWRITE", "omni_expert_counts", "omni_balance_fwd_workspace_size",
     "omni_balance_fwd", "omni_balance_bwd_workspace_size", "omni_balance_bwd",
     "omni_layer_norm_fwd", "omni_layer_norm_bwd_workspace_size", "omni_layer_norm_bwd",
     "omni_act_pack", "omni_act_unpack", "omni_routed_bwd_ckpt_workspace_size",
@@ -185,74 +185,128 @@ def layer_fwd(x, W, V, W_r, W_c, W_g, W_u, W_d, K, B, y=None, ws=None, mlp_ws=No
 
 
 # ------------------------------------------------------- training operators
+# These run once or more per layer and step, some of them for a few
+# microseconds, so their checks read each attribute once and the C entry point
+# gets plain addresses.
 
 _BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 
 
-def _need(name, t, dtypes, shape, dev=None):
-    """ValueError unless t is a contiguous CUDA tensor of one of the types and
-    of this shape (on `dev`, if given)."""
+def _refuse(name, t, dtype, shape, di):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name}: a CUDA tensor is expected")
-    if t.dtype not in (dtypes if isinstance(dtypes, tuple) else (dtypes,)):
-        raise ValueError(f"{name}: {dtypes} expected, got {t.dtype}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: {dtype} expected, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(shape)} expected, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: a contiguous tensor is expected")
-    if dev is not None and t.device != dev:
-        raise ValueError(f"{name}: on {t.device}, the other tensors on {dev}")
-    return t
+    if t.get_device() != di:
+        raise ValueError(f"{name}: on cuda:{t.get_device()}, the other tensors on cuda:{di}")
+    raise ValueError(f"{name}: a contiguous tensor is expected")
 
 
-def _shape(name, t, dims):
-    if not isinstance(t, torch.Tensor) or t.dim() != dims:
-        raise ValueError(f"{name}: a tensor of {dims} dimensions is expected")
-    return t.shape
+def _at(name, t, dtype, shape, di):
+    """Address of t; ValueError unless it is a contiguous tensor of this type
+    and shape on device di."""
+    try:
+        if (t.dtype is dtype and t.shape == shape and t.get_device() == di and t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:                              # no tensor
+        pass
+    _refuse(name, t, dtype, shape, di)
+
+
+def _rows(name, t):
+    """Shape [rows, columns] and device index of a CUDA matrix."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{name}: a tensor of 2 dimensions is expected")
+    di = t.get_device()
+    if di < 0:
+        raise ValueError(f"{name}: a CUDA tensor is expected")
+    return (*t.shape, di)
+
+
+def _bf16_or_f32(name, t, shape, di):
+    """Address and OMNI_X_F32 flag of a bf16 or fp32 tensor."""
+    if isinstance(t, torch.Tensor) and t.dtype is _F32:
+        return _at(name, t, _F32, shape, di), OMNI_X_F32
+    return _at(name, t, _BF16, shape, di), 0
+
+
+def _mask_at(mask, L, di):
+    if mask is None:
+        return None
+    bits = isinstance(mask, torch.Tensor) and mask.dtype is torch.bool
+    return _at("mask", mask, torch.bool if bits else _U8, (L,), di)
+
+
+def _elsewhere(di, stream):
+    """Whether a call has to change the current device or stream first."""
+    if stream is not None:
+        if stream.device.index != di:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{di}")
+        return True
+    return torch.cuda.current_device() != di
 
 
 @contextlib.contextmanager
-def _switched(dev, stream):
-    with torch.cuda.device(dev):
+def _on(di, stream):
+    """Makes the tensors' device current, and `stream` where one is given, for
+    the allocations and launches of a call."""
+    with torch.cuda.device(di):
         with torch.cuda.stream(stream):
             yield
 
 
-def _on(dev, stream):
-    """Makes the tensors' device current, and `stream` (default: that device's
-    current one), for the allocations and launches of a call."""
-    if stream is not None:
-        if stream.device != dev:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
-        return _switched(dev, stream)
-    if torch.cuda.current_device() != dev.index:
-        return torch.cuda.device(dev)
-    return contextlib.nullcontext()
+def _new(n, dtype, di):
+    return torch.empty(n, dtype=dtype, device=di)
 
 
-def _scratch(ws, n, dev):
+def _scratch(ws, n, di):
+    """Workspace, its address and its size."""
     if ws is None:
-        return torch.empty(n, dtype=_U8, device=dev)
-    return _need("ws", ws, _U8, (ws.numel(),), dev)
+        ws = torch.empty(n, dtype=_U8, device=di)
+        return ws, ws.data_ptr(), n
+    n = ws.numel() if isinstance(ws, torch.Tensor) else 0
+    return ws, _at("ws", ws, _U8, (n,), di), n
 
 
-def _token_mask(mask, L, dev):
-    if mask is None:
-        return None
-    return _need("mask", mask, (torch.bool, _U8), (L,), dev)
+# the current stream's handle without a Stream object around it, where torch has that
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _queue(di):
+    return _raw_stream(di) if _raw_stream else torch.cuda.current_stream(di).cuda_stream
+
+
+def _grad(name, g, like):
+    """An fp32 gradient to accumulate into: the given one, or a zeroed one."""
+    if g is None:
+        return torch.zeros_like(like, dtype=_F32)
+    _at(name, g, _F32, like.shape, like.get_device())
+    return g
+
+
+def _grads(names, given, like):
+    """The weight gradients to write: the given fp32 buffers, which are
+    accumulated into, or new ones.  All new: OMNI_DW_OVERWRITE spares zeroing
+    and reading them; some given: the new ones start at zero."""
+    if given[0] is None and given[-1] is None:
+        return [torch.empty_like(t, dtype=_F32) for t in like], OMNI_DW_OVERWRITE
+    return [_grad(*ngl) for ngl in zip(names, given, like)], 0
 
 
 def expert_counts(idx, N, mask=None, ws=None, stream=None):
     """Tasks per expert and kept tokens: counts [N] and n_tokens [1], int32.
     idx [L, K] int32; mask [L] bool or uint8, None = every token counts."""
-    L, K = _shape("idx", idx, 2)
-    dev = _need("idx", idx, _I32, (L, K)).device
-    mask = _token_mask(mask, L, dev)
-    with _on(dev, stream):
-        counts = torch.empty(max(N, 0), dtype=_I32, device=dev)
-        n_tokens = torch.empty(1, dtype=_I32, device=dev)
-        ws = _scratch(ws, 256, dev)
-        omni_expert_counts(idx, mask, L, K, N, counts, n_tokens, ws)
+    L, K, di = _rows("idx", idx)
+    if _elsewhere(di, stream):
+        with _on(di, stream):
+            return expert_counts(idx, N, mask, ws)
+    counts, n_tokens = _new(max(N, 0), _I32, di), _new(1, _I32, di)
+    ws, ws_at, ws_n = _scratch(ws, 256, di)
+    _check("omni_expert_counts", load().omni_expert_counts(
+        _at("idx", idx, _I32, (L, K), di), _mask_at(mask, L, di), L, K, N, counts.data_ptr(),
+        n_tokens.data_ptr(), ws_at, ws_n, _queue(di)))
     return dict(counts=counts, n_tokens=n_tokens)
 
 
@@ -260,17 +314,19 @@ def balance_fwd(p_r, p_c, counts, n_tokens, K, mask=None, ws=None, stream=None):
     """Balance loss of the router: loss (0-dim) and token_loss [L], fp32.
     p_r, p_c: log-probabilities (router_topk's); counts, n_tokens from
     expert_counts."""
-    (L, N_r), (_, N_c) = _shape("p_r", p_r, 2), _shape("p_c", p_c, 2)
-    dev = _need("p_r", p_r, _F32, (L, N_r)).device
-    _need("p_c", p_c, _F32, (L, N_c), dev)
-    _need("counts", counts, _I32, (N_r * N_c,), dev)
-    _need("n_tokens", n_tokens, _I32, (1,), dev)
-    mask = _token_mask(mask, L, dev)
-    with _on(dev, stream):
-        loss = torch.empty((), dtype=_F32, device=dev)
-        token_loss = torch.empty(L, dtype=_F32, device=dev)
-        ws = _scratch(ws, omni_balance_fwd_workspace_size(L, N_r, N_c), dev)
-        omni_balance_fwd(p_r, p_c, counts, n_tokens, mask, L, N_r, N_c, K, loss, token_loss, ws)
+    L, N_r, di = _rows("p_r", p_r)
+    N_c = _rows("p_c", p_c)[1]
+    if _elsewhere(di, stream):
+        with _on(di, stream):
+            return balance_fwd(p_r, p_c, counts, n_tokens, K, mask, ws)
+    at = (_at("p_r", p_r, _F32, (L, N_r), di), _at("p_c", p_c, _F32, (L, N_c), di),
+          _at("counts", counts, _I32, (N_r * N_c,), di), _at("n_tokens", n_tokens, _I32, (1,), di),
+          _mask_at(mask, L, di))
+    loss, token_loss = _new((), _F32, di), _new(L, _F32, di)
+    lib = load()
+    ws, ws_at, ws_n = _scratch(ws, lib.omni_balance_fwd_workspace_size(L, N_r, N_c), di)
+    _check("omni_balance_fwd", lib.omni_balance_fwd(
+        *at, L, N_r, N_c, K, loss.data_ptr(), token_loss.data_ptr(), ws_at, ws_n, _queue(di)))
     return dict(loss=loss, token_loss=token_loss)
 
 
@@ -278,31 +334,29 @@ def balance_bwd(x, W_r, W_c, p_r, p_c, counts, n_tokens, K, token_loss, dloss=1.
                 dx=None, dW_r=None, dW_c=None, ws=None, stream=None):
     """Gradients of dloss * balance loss.  With a given dx the gradient is
     added to it (routed_bwd's dx), else a new one is returned; dW_r, dW_c are
-    accumulated into the given fp32 buffers (new zeroed ones if None)."""
-    (L, d), (N_r, _), (N_c, _) = _shape("x", x, 2), _shape("W_r", W_r, 2), _shape("W_c", W_c, 2)
-    dev = _need("x", x, _BF16, (L, d)).device
-    _need("W_r", W_r, _BF16, (N_r, d), dev)
-    _need("W_c", W_c, _BF16, (N_c, d), dev)
-    _need("p_r", p_r, _F32, (L, N_r), dev)
-    _need("p_c", p_c, _F32, (L, N_c), dev)
-    _need("counts", counts, _I32, (N_r * N_c,), dev)
-    _need("n_tokens", n_tokens, _I32, (1,), dev)
-    _need("token_loss", token_loss, _F32, (L,), dev)
-    mask = _token_mask(mask, L, dev)
-    flags = 0
-    with _on(dev, stream):
-        if dx is None:
-            dx = torch.empty((L, d), dtype=_F32, device=dev)
-        else:
-            _need("dx", dx, _F32, (L, d), dev)
-            flags = OMNI_DX_ACCUMULATE
-        dW_r = torch.zeros((N_r, d), dtype=_F32, device=dev) if dW_r is None else \
-            _need("dW_r", dW_r, _F32, (N_r, d), dev)
-        dW_c = torch.zeros((N_c, d), dtype=_F32, device=dev) if dW_c is None else \
-            _need("dW_c", dW_c, _F32, (N_c, d), dev)
-        ws = _scratch(ws, omni_balance_bwd_workspace_size(L, d, N_r, N_c), dev)
-        omni_balance_bwd(x, W_r, W_c, p_r, p_c, counts, n_tokens, mask, token_loss, L, d, N_r, N_c,
-                         K, float(dloss), dx, dW_r, dW_c, flags, ws)
+    accumulated into the given fp32 buffers (new ones if None)."""
+    L, d, di = _rows("x", x)
+    N_r, N_c = _rows("W_r", W_r)[0], _rows("W_c", W_c)[0]
+    if _elsewhere(di, stream):
+        with _on(di, stream):
+            return balance_bwd(x, W_r, W_c, p_r, p_c, counts, n_tokens, K, token_loss, dloss, mask,
+                               dx, dW_r, dW_c, ws)
+    at = (_at("x", x, _BF16, (L, d), di), _at("W_r", W_r, _BF16, (N_r, d), di),
+          _at("W_c", W_c, _BF16, (N_c, d), di), _at("p_r", p_r, _F32, (L, N_r), di),
+          _at("p_c", p_c, _F32, (L, N_c), di), _at("counts", counts, _I32, (N_r * N_c,), di),
+          _at("n_tokens", n_tokens, _I32, (1,), di), _mask_at(mask, L, di),
+          _at("token_loss", token_loss, _F32, (L,), di))
+    (dW_r, dW_c), flags = _grads(("dW_r", "dW_c"), (dW_r, dW_c), (W_r, W_c))
+    if dx is None:
+        dx = torch.empty_like(x, dtype=_F32)
+    else:
+        _at("dx", dx, _F32, (L, d), di)
+        flags |= OMNI_DX_ACCUMULATE
+    lib = load()
+    ws, ws_at, ws_n = _scratch(ws, lib.omni_balance_bwd_workspace_size(L, d, N_r, N_c), di)
+    _check("omni_balance_bwd", lib.omni_balance_bwd(
+        *at, L, d, N_r, N_c, K, float(dloss), dx.data_ptr(), dW_r.data_ptr(), dW_c.data_ptr(), flags,
+        ws_at, ws_n, _queue(di)))
     return dict(dx=dx, dW_r=dW_r, dW_c=dW_c)
 
 
@@ -311,21 +365,25 @@ def layer_norm_fwd(x, w, b=None, eps=1e-5, ckpt=False, stats=True, stream=None):
     optional bias b (bf16): y bf16, with stats also mean and rstd [L] fp32,
     with ckpt also the 8-bit checkpoint (q [L, d], scale [L, d / 32], uint8) of
     the rows before w and b."""
-    L, d = _shape("x", x, 2)
-    dev = _need("x", x, (_BF16, _F32), (L, d)).device
-    _need("w", w, _BF16, (d,), dev)
-    if b is not None:
-        _need("b", b, _BF16, (d,), dev)
-    with _on(dev, stream):
-        out = dict(y=torch.empty((L, d), dtype=_BF16, device=dev))
-        if stats:
-            out |= dict(mean=torch.empty(L, dtype=_F32, device=dev),
-                        rstd=torch.empty(L, dtype=_F32, device=dev))
-        if ckpt:
-            out |= dict(q=torch.empty((L, d), dtype=_U8, device=dev),
-                        scale=torch.empty((L, d // 32), dtype=_U8, device=dev))
-        omni_layer_norm_fwd(x, w, b, L, d, eps, out["y"], out.get("mean"), out.get("rstd"),
-                            out.get("q"), out.get("scale"), OMNI_X_F32 if x.dtype == _F32 else 0)
+    L, d, di = _rows("x", x)
+    if _elsewhere(di, stream):
+        with _on(di, stream):
+            return layer_norm_fwd(x, w, b, eps, ckpt, stats)
+    x_at, flags = _bf16_or_f32("x", x, (L, d), di)
+    y = torch.empty_like(x, dtype=_BF16)
+    out = dict(y=y)
+    at = [None, None, None, None]
+    if stats:
+        out["mean"] = mean = _new(L, _F32, di)
+        out["rstd"] = rstd = _new(L, _F32, di)
+        at[:2] = mean.data_ptr(), rstd.data_ptr()
+    if ckpt:
+        out["q"] = q = torch.empty_like(x, dtype=_U8)
+        out["scale"] = scale = torch.empty(L, d // 32, dtype=_U8, device=di)
+        at[2:] = q.data_ptr(), scale.data_ptr()
+    _check("omni_layer_norm_fwd", load().omni_layer_norm_fwd(
+        x_at, _at("w", w, _BF16, (d,), di), None if b is None else _at("b", b, _BF16, (d,), di), L,
+        d, eps, y.data_ptr(), *at, flags, _queue(di)))
     return out
 
 
@@ -334,63 +392,68 @@ def layer_norm_bwd(dy, w, rstd, x=None, mean=None, q=None, scale=None, bias=True
     """Backward of layer_norm_fwd from its kept input (x, mean) or from its
     checkpoint (q, scale).  With a given dx the gradient is added to it (the
     residual's), else a new one is returned; dw and (with bias) db are
-    accumulated into the given fp32 buffers (new zeroed ones if None)."""
-    L, d = _shape("dy", dy, 2)
-    dev = _need("dy", dy, _F32, (L, d)).device
-    _need("w", w, _BF16, (d,), dev)
-    _need("rstd", rstd, _F32, (L,), dev)
-    flags = 0
-    if q is not None:
-        if x is not None:
-            raise ValueError("x and q: one of the two is expected")
-        _need("q", q, _U8, (L, d), dev)
-        _need("scale", scale, _U8, (L, d // 32), dev)
-        mean = None
+    accumulated into the given fp32 buffers (new ones if None)."""
+    L, d, di = _rows("dy", dy)
+    if (q is not None and x is not None) or (db is not None and not bias):
+        raise ValueError("one of x and q, and db only with bias")
+    if _elsewhere(di, stream):
+        with _on(di, stream):
+            return layer_norm_bwd(dy, w, rstd, x, mean, q, scale, bias, dx, dw, db, ws)
+    w_at = _at("w", w, _BF16, (d,), di)
+    dy_at = _at("dy", dy, _F32, (L, d), di)
+    if bias:
+        (dw, db), flags = _grads(("dw", "db"), (dw, db), (w, w))
     else:
-        _need("x", x, (_BF16, _F32), (L, d), dev)
-        _need("mean", mean, _F32, (L,), dev)
-        flags = OMNI_X_F32 if x.dtype == _F32 else 0
-    if db is not None and not bias:
-        raise ValueError("db without bias")
-    with _on(dev, stream):
-        if dx is None:
-            dx = torch.empty((L, d), dtype=_F32, device=dev)
-        else:
-            _need("dx", dx, _F32, (L, d), dev)
-            flags |= OMNI_DX_ACCUMULATE
-        dw = torch.zeros(d, dtype=_F32, device=dev) if dw is None else \
-            _need("dw", dw, _F32, (d,), dev)
-        if bias:
-            db = torch.zeros(d, dtype=_F32, device=dev) if db is None else \
-                _need("db", db, _F32, (d,), dev)
-        ws = _scratch(ws, omni_layer_norm_bwd_workspace_size(L, d), dev)
-        omni_layer_norm_bwd(x, mean, rstd, q, scale, w, dy, L, d, dx, dw, db, flags, ws)
+        (dw,), flags = _grads(("dw",), (dw,), (w,))
+    x_at = mean_at = q_at = scale_at = None
+    if q is not None:
+        q_at = _at("q", q, _U8, (L, d), di)
+        scale_at = _at("scale", scale, _U8, (L, d // 32), di)
+    else:
+        x_at, x_flag = _bf16_or_f32("x", x, (L, d), di)
+        mean_at = _at("mean", mean, _F32, (L,), di)
+        flags |= x_flag
+    if dx is None:
+        dx = torch.empty_like(dy)
+    else:
+        _at("dx", dx, _F32, (L, d), di)
+        flags |= OMNI_DX_ACCUMULATE
+    lib = load()
+    ws, ws_at, ws_n = _scratch(ws, lib.omni_layer_norm_bwd_workspace_size(L, d), di)
+    _check("omni_layer_norm_bwd", lib.omni_layer_norm_bwd(
+        x_at, mean_at, _at("rstd", rstd, _F32, (L,), di), q_at, scale_at, w_at, dy_at, L, d,
+        dx.data_ptr(), dw.data_ptr(), db.data_ptr() if bias else None, flags, ws_at, ws_n,
+        _queue(di)))
     return dict(dx=dx, dw=dw, db=db)
 
 
 def act_pack(x, stream=None):
     """8-bit checkpoint of x [L, d] (bf16 or fp32): q [L, d] e4m3 bytes and
     scale [L, d / 32] bytes; the values are q * 2**(scale - 127)."""
-    L, d = _shape("x", x, 2)
-    dev = _need("x", x, (_BF16, _F32), (L, d)).device
-    with _on(dev, stream):
-        q = torch.empty((L, d), dtype=_U8, device=dev)
-        scale = torch.empty((L, d // 32), dtype=_U8, device=dev)
-        omni_act_pack(x, L, d, q, scale, OMNI_X_F32 if x.dtype == _F32 else 0)
+    L, d, di = _rows("x", x)
+    if _elsewhere(di, stream):
+        with _on(di, stream):
+            return act_pack(x)
+    x_at, flags = _bf16_or_f32("x", x, (L, d), di)
+    q = torch.empty_like(x, dtype=_U8)
+    scale = torch.empty(L, d // 32, dtype=_U8, device=di)
+    _check("omni_act_pack", load().omni_act_pack(x_at, L, d, q.data_ptr(), scale.data_ptr(), flags,
+                                                 _queue(di)))
     return q, scale
 
 
 def act_unpack(q, scale, w=None, b=None, stream=None):
     """The values of a checkpoint, times w and plus b where given, as bf16."""
-    L, d = _shape("q", q, 2)
-    dev = _need("q", q, _U8, (L, d)).device
-    _need("scale", scale, _U8, (L, d // 32), dev)
-    for name, t in (("w", w), ("b", b)):
-        if t is not None:
-            _need(name, t, _BF16, (d,), dev)
-    with _on(dev, stream):
-        y = torch.empty((L, d), dtype=_BF16, device=dev)
-        omni_act_unpack(q, scale, w, b, L, d, y)
+    L, d, di = _rows("q", q)
+    if _elsewhere(di, stream):
+        with _on(di, stream):
+            return act_unpack(q, scale, w, b)
+    q_at = _at("q", q, _U8, (L, d), di)
+    y = torch.empty_like(q, dtype=_BF16)
+    _check("omni_act_unpack", load().omni_act_unpack(
+        q_at, _at("scale", scale, _U8, (L, d // 32), di),
+        None if w is None else _at("w", w, _BF16, (d,), di),
+        None if b is None else _at("b", b, _BF16, (d,), di), L, d, y.data_ptr(), _queue(di)))
     return y
 
 
@@ -398,27 +461,26 @@ def routed_bwd_ckpt(q, scale, W, V, W_r, W_c, idx, gate, dy, w=None, b=None, dW=
                     dW_r=None, dW_c=None, ws=None, stream=None):
     """routed_bwd with its tokens restored from a checkpoint,
     x = act_unpack(q, scale, w, b)."""
-    (L, d), (N_r, _), (N_c, _) = _shape("q", q, 2), _shape("W_r", W_r, 2), _shape("W_c", W_c, 2)
-    K = _shape("idx", idx, 2)[1]
-    dev = _need("q", q, _U8, (L, d)).device
-    _need("scale", scale, _U8, (L, d // 32), dev)
-    for name, t in (("w", w), ("b", b)):
-        if t is not None:
-            _need(name, t, _BF16, (d,), dev)
-    weights = dict(W=(W, N_r * N_c), V=(V, N_r * N_c), W_r=(W_r, N_r), W_c=(W_c, N_c))
-    for name, (t, rows) in weights.items():
-        _need(name, t, _BF16, (rows, d), dev)
-    _need("idx", idx, _I32, (L, K), dev)
-    _need("gate", gate, _F32, (L, K), dev)
-    _need("dy", dy, _F32, (L, d), dev)
-    with _on(dev, stream):
-        dx = torch.empty((L, d), dtype=_F32, device=dev)
-        grads = dict(dW=dW, dV=dV, dW_r=dW_r, dW_c=dW_c)
-        for name, g in grads.items():
-            shape = weights[name[1:]][0].shape
-            grads[name] = torch.zeros(shape, dtype=_F32, device=dev) if g is None else \
-                _need(name, g, _F32, shape, dev)
-        ws = _scratch(ws, omni_routed_bwd_ckpt_workspace_size(L, d, N_r, N_c, K), dev)
-        omni_routed_bwd_ckpt(q, scale, w, b, W, V, W_r, W_c, L, d, N_r, N_c, K, idx, gate, dy, dx,
-                             grads["dW"], grads["dV"], grads["dW_r"], grads["dW_c"], 0, ws)
-    return dict(dx=dx, **grads)
+    L, d, di = _rows("q", q)
+    N_r, N_c, K = _rows("W_r", W_r)[0], _rows("W_c", W_c)[0], _rows("idx", idx)[1]
+    if _elsewhere(di, stream):
+        with _on(di, stream):
+            return routed_bwd_ckpt(q, scale, W, V, W_r, W_c, idx, gate, dy, w, b, dW, dV, dW_r,
+                                   dW_c, ws)
+    N = N_r * N_c
+    at = (_at("q", q, _U8, (L, d), di), _at("scale", scale, _U8, (L, d // 32), di),
+          None if w is None else _at("w", w, _BF16, (d,), di),
+          None if b is None else _at("b", b, _BF16, (d,), di), _at("W", W, _BF16, (N, d), di),
+          _at("V", V, _BF16, (N, d), di), _at("W_r", W_r, _BF16, (N_r, d), di),
+          _at("W_c", W_c, _BF16, (N_c, d), di), L, d, N_r, N_c, K,
+          _at("idx", idx, _I32, (L, K), di), _at("gate", gate, _F32, (L, K), di),
+          _at("dy", dy, _F32, (L, d), di))
+    dx = torch.empty_like(dy)
+    dW, dV = _grad("dW", dW, W), _grad("dV", dV, V)
+    dW_r, dW_c = _grad("dW_r", dW_r, W_r), _grad("dW_c", dW_c, W_c)
+    lib = load()
+    ws, ws_at, ws_n = _scratch(ws, lib.omni_routed_bwd_ckpt_workspace_size(L, d, N_r, N_c, K), di)
+    _check("omni_routed_bwd_ckpt", lib.omni_routed_bwd_ckpt(
+        *at, dx.data_ptr(), dW.data_ptr(), dV.data_ptr(), dW_r.data_ptr(), dW_c.data_ptr(), 0, ws_at,
+        ws_n, _queue(di)))
+    return dict(dx=dx, dW=dW, dV=dV, dW_r=dW_r, dW_c=dW_c)

@@ -24,6 +24,7 @@ OMNI_EXPERT_DENSE = 16
 OMNI_EXPERT_SPARSE = 32
 OMNI_X_F32 = 64
 OMNI_DX_ACCUMULATE = 128
+OMNI_DW_OVERWRITE = 256
 
 STATUS = {0: "OMNI_OK", -1: "OMNI_ERR_INVALID_ARG", -2: "OMNI_ERR_UNSUPPORTED",
           -3: "OMNI_ERR_WORKSPACE", -4: "OMNI_ERR_CUDA", -5: "OMNI_ERR_DEVICE"}

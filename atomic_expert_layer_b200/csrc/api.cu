@@ -595,12 +595,11 @@ int omni_expert_counts(const int32_t *idx, const uint8_t *mask, int L, int K, in
         return OMNI_ERR_INVALID_ARG;
     if ((int64_t)L * K > INT_MAX) return OMNI_ERR_UNSUPPORTED;
     if (!aligned4(idx) || !aligned4(counts) || !aligned4(n_tokens)) return OMNI_ERR_INVALID_ARG;
-    int rc = check_plain_ws(ws, ws_bytes, sizeof(WsHeader));
+    const int rc = check_plain_ws(ws, ws_bytes, sizeof(WsHeader));
     if (rc) return rc;
-    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if ((rc = clear_header(ws, st))) return rc;
+    first_launch_in_call();
     return cuda_rc(launch_counts(idx, mask, (int64_t)L * K, K, N, counts, n_tokens,
-                                 ws_at<int>(ws, 0), st));
+                                 ws_at<int>(ws, 0), reinterpret_cast<cudaStream_t>(stream)));
 }
 
 size_t omni_balance_fwd_workspace_size(int L, int N_r, int N_c) {
@@ -639,7 +638,8 @@ int omni_balance_bwd(const omni_bf16 *x, const omni_bf16 *W_r, const omni_bf16 *
                      omni_stream_t stream) {
     int rc = check_grid(L, N_r, N_c, K);
     if (rc) return rc;
-    if (d <= 0 || (flags & ~OMNI_DX_ACCUMULATE) != 0) return OMNI_ERR_INVALID_ARG;
+    if (d <= 0 || (flags & ~(OMNI_DX_ACCUMULATE | OMNI_DW_OVERWRITE)) != 0)
+        return OMNI_ERR_INVALID_ARG;
     if (!x || !W_r || !W_c || !p_r || !p_c || !counts || !n_tokens || !token_loss || !dx ||
         !dW_r || !dW_c || !ws)
         return OMNI_ERR_INVALID_ARG;
@@ -654,7 +654,7 @@ int omni_balance_bwd(const omni_bf16 *x, const omni_bf16 *W_r, const omni_bf16 *
     if ((rc = clear_header(ws, st))) return rc;
     return cuda_rc(launch_balance_bwd(x, W_r, W_c, p_r, p_c, counts, n_tokens, mask, token_loss, L,
                                       d, N_r, N_c, K, dloss, dx, (flags & OMNI_DX_ACCUMULATE) != 0,
-                                      dW_r, dW_c, ws, st));
+                                      dW_r, dW_c, (flags & OMNI_DW_OVERWRITE) != 0, ws, st));
 }
 
 int omni_layer_norm_fwd(const void *x, const omni_bf16 *w, const omni_bf16 *b, int L, int d,
@@ -683,7 +683,8 @@ int omni_layer_norm_bwd(const void *x, const float *mean, const float *rstd, con
                         omni_stream_t stream) {
     int rc = check_norm(L, d, q != nullptr);
     if (rc) return rc;
-    if ((flags & ~(OMNI_X_F32 | OMNI_DX_ACCUMULATE)) != 0) return OMNI_ERR_INVALID_ARG;
+    if ((flags & ~(OMNI_X_F32 | OMNI_DX_ACCUMULATE | OMNI_DW_OVERWRITE)) != 0)
+        return OMNI_ERR_INVALID_ARG;
     if (!rstd || !w || !dy || !dx || !dw || !ws || !q != !scale || (!q && (!x || !mean)))
         return OMNI_ERR_INVALID_ARG;
     if (!aligned16(x) || !aligned16(q) || !aligned16(w) || !aligned16(dy) || !aligned16(dx) ||
@@ -693,6 +694,7 @@ int omni_layer_norm_bwd(const void *x, const float *mean, const float *rstd, con
     first_launch_in_call();
     return cuda_rc(launch_norm_bwd(x, (flags & OMNI_X_F32) != 0, mean, rstd, q, scale, w, dy, L, d,
                                    dx, (flags & OMNI_DX_ACCUMULATE) != 0, dw, db,
+                                   (flags & OMNI_DW_OVERWRITE) != 0,
                                    ws_at<float>(ws, sizeof(WsHeader)),
                                    reinterpret_cast<cudaStream_t>(stream)));
 }

@@ -17,19 +17,21 @@
 //   ds_r[t, i] = c P_r[t, i] (U[t, i] - l_t),  ds_c[t, j] = c P_c[t, j] (V[t, j] - l_t),
 //   dx = ds_r W_r + ds_c W_c,  dW_r += ds_r^T x,  dW_c += ds_c^T x.
 //
-// All products run as tcgen05 tile GEMMs with fp32 accumulation.  An operand
-// that is fp32 by nature enters as the sum of two 16-bit values, hi + lo,
-// against one that 16 bits hold exactly; both halves meet the same B tile, so
-// it is loaded once.
-//   U, V: fp16.  2^14 P keeps 22 bits (or 2^-39 of P, whichever is coarser)
-//     and 2^-16 F holds counts up to 2048 exactly.  U - l_t cancels when the
-//     experts are nearly even or when the router has collapsed; bf16 halves
-//     (16 bits) left ds of a collapsed router off by 4e-3 where these leave
-//     what fp32 arithmetic does.  When some count exceeds 2048, what its
-//     rounding to fp16 leaves is a second matrix F_lo, and hi * F_lo is added
-//     (22 bits of a count).
-//   dx, dW: bf16, the type of W and x.  ds is off by at most 2^-16 of itself
-//     (one bf16 would lose 2^-8).
+// All products run as fp16 tcgen05 tile GEMMs with fp32 accumulation on CTA
+// pairs.  An operand that is fp32 by nature (P, ds) enters as the sum of two
+// fp16 values, hi + lo (22 bits), against one that fp16 holds exactly; both
+// halves meet the same B tile, so it is loaded once.  Powers of two keep the
+// operands inside fp16's range, and come out again in the epilogue:
+//   P by 2^14 (22 bits, or 2^-39 of 1 where that is coarser);
+//   counts by 2^-16: exact up to 2048.  When some count is larger, what its
+//     rounding leaves is a second matrix F_lo, and hi * F_lo is added;
+//   ds / c = P (U - l_t), whose magnitude no more than the largest count
+//     bounds, so that this bound becomes 2^15;
+//   x and W, bf16: so that their largest finite magnitude becomes 2^14 to
+//     2^15.  fp16 then holds every bf16 value down to 2^-32 of it exactly.
+// bf16 halves (16 bits) need no scales, but left dx and dW off by 2.9e-6 of
+// themselves, and by 4e-3 for a collapsed router, where U - l_t cancels; fp32
+// arithmetic leaves 1e-6 and 2e-4 there.
 //
 // Masked rows of p are never read as numbers: their P and ds are zero.
 #include <cuda_bf16.h>
@@ -42,34 +44,12 @@
 namespace omni {
 namespace {
 
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&v);
-}
-__device__ __forceinline__ float bf16_of(float v) { return __bfloat162float(__float2bfloat16_rn(v)); }
-
-// 8 values as hi and lo bf16 vectors
-__device__ __forceinline__ void split8(const float *v, uint4 *hi, uint4 *lo) {
-    uint32_t h[4], l[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float a = v[2 * i], b = v[2 * i + 1];
-        const float ah = bf16_of(a), bh = bf16_of(b);
-        h[i] = pack_bf16(ah, bh);
-        l[i] = pack_bf16(a - ah, b - bh);
-    }
-    *hi = make_uint4(h[0], h[1], h[2], h[3]);
-    *lo = make_uint4(l[0], l[1], l[2], l[3]);
-}
-
 // The scales at which P and the counts are held in fp16.
 constexpr float kScaleP = 16384.f;              // 2^14
 constexpr float kScaleF = 1.f / 65536.f;        // 2^-16: counts up to 2^31 stay below fp16's largest
 constexpr float kUnscale = 4.f;                 // 1 / (kScaleP kScaleF)
 constexpr int kExactCount = 2048;               // counts up to this need no F_lo
 
-__device__ __forceinline__ float f16_of(float v) { return __half2float(__float2half_rn(v)); }
-__device__ __forceinline__ uint16_t f16_bits(float v) { return __half_as_ushort(__float2half_rn(v)); }
 __device__ __forceinline__ void split8_f16(const float *v, uint4 *hi, uint4 *lo) {
     uint32_t h[4], l[4];
 #pragma unroll
@@ -84,36 +64,66 @@ __device__ __forceinline__ void split8_f16(const float *v, uint4 *hi, uint4 *lo)
     *lo = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
+// Words of the workspace header after the status (all zero when a call starts).
+struct BalHeader {
+    int status;
+    int most;            // largest count
+    int kept;            // tokens of this batch with mask != 0
+    int done;            // CTAs that have finished (forward)
+    uint32_t x_top;      // largest finite magnitude of the kept rows of x, as bits
+    uint32_t w_top;      // ... of W_r and W_c
+};
+// Exponent that takes a magnitude below 2^15 (its bits as fp32, subnormals
+// and numbers below 2^-60 as 2^-60), and the two powers of two.
+__device__ __forceinline__ int top_exp(uint32_t bits) {
+    const int e = (int)(bits >> 23) - 127;
+    return 14 - (e < -60 ? -60 : e);
+}
+__device__ __forceinline__ float pow2f(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+// P (U - l) / 2^count_exp is below 1
+__device__ __forceinline__ int count_exp(int most) { return 32 - __clz(most); }
+
 // ----------------------------------------------------------------- counts
 __global__ void counts_clear_kernel(int32_t *__restrict__ counts, int64_t N,
-                                    int32_t *__restrict__ n_tokens) {
+                                    int32_t *__restrict__ n_tokens, int *status) {
     grid_dependency_wait();
     grid_dependents_launch();
     const int64_t at = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+#pragma unroll 4
     for (int64_t i = at; i < N; i += (int64_t)gridDim.x * blockDim.x) counts[i] = 0;
-    if (at == 0) *n_tokens = 0;
+    if (at == 0) {
+        *n_tokens = 0;
+        *status = OMNI_DEV_OK;
+    }
 }
 
+constexpr int kCountSpan = 4096;        // mask bytes that a CTA counts at a time
+
 // One thread per task; integer atomics, so the counts do not depend on the
-// order.  The thread of a kept token's first task counts the token.
+// order.  Kept tokens are counted from the mask, 4096 by a CTA: an atomic per
+// token, all on one address, took 60 us of 67 at 16384 tokens.
 __global__ void __launch_bounds__(256)
-counts_kernel(const int32_t *__restrict__ idx, const uint8_t *__restrict__ mask, int64_t M, int K,
-              int64_t N, int32_t *__restrict__ counts, int32_t *__restrict__ n_tokens, int *status) {
+counts_kernel(const int32_t *__restrict__ idx, const uint8_t *__restrict__ mask, int M, int K, int N,
+              int32_t *__restrict__ counts, int32_t *__restrict__ n_tokens, int *status) {
     grid_dependency_wait();
     grid_dependents_launch();
-    const int64_t m = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    bool first = false;
-    if (m < M) {
-        const int64_t t = m / K;
-        if (!mask || mask[t]) {
-            const int e = idx[m];
-            if (e < 0 || e >= N) set_status(status, OMNI_DEV_BAD_EXPERT);
-            else atomicAdd(&counts[e], 1);
-            first = m == t * K;
-        }
+    const unsigned at = blockIdx.x * 256 + threadIdx.x;       // M < 2^31: no wrap
+    if (at < (unsigned)M && (!mask || mask[at / (unsigned)K])) {
+        const int e = idx[at];
+        if (e >= 0 && e < N) atomicAdd(&counts[e], 1);
+        else set_status(status, OMNI_DEV_BAD_EXPERT);
     }
-    const unsigned votes = __ballot_sync(0xffffffffu, first);
-    if (votes && lane_id() == 0) atomicAdd(n_tokens, __popc(votes));
+    const int L = M / K;
+    if (!mask) {
+        if (at == 0) *n_tokens = L;
+        return;
+    }
+    const int64_t t0 = (int64_t)blockIdx.x * kCountSpan;
+    if (t0 >= L) return;
+    int kept = 0;
+    for (int i = (int)threadIdx.x; i < kCountSpan && t0 + i < L; i += 256) kept += mask[t0 + i] != 0;
+    kept = warp_isum(kept);
+    if (kept && lane_id() == 0) atomicAdd(n_tokens, kept);
 }
 
 // -------------------------------------------------------------- operands
@@ -121,106 +131,266 @@ struct BalPrep {
     const float *p_r, *p_c;
     const int32_t *counts;
     const uint8_t *mask;
-    const uint16_t *x;            // masked copy wanted when xs is not null
+    const uint16_t *x, *W_r, *W_c;   // backward (else null): their largest magnitudes are wanted
     int L, N_r, N_c, d;
     int seg_r, ld;                // columns of the row segment, and of P (0: only the column axis)
     int pc, pr;                   // padded N_c, N_r
-    uint16_t *P_hi, *P_lo, *F_hi, *F_lo, *T_hi, *T_lo, *xs;
-    int *big;                     // set when a count exceeds kExactCount
-    int *n_local;                 // kept tokens of this batch
+    uint16_t *P_hi, *P_lo, *F_hi, *F_lo, *T_hi, *T_lo;
+    BalHeader *hdr;
 };
 
-__device__ __forceinline__ void prep_probs(const BalPrep &p, int64_t unit) {
-    const int per = p.ld >> 3;
-    const int64_t t = unit / per;
-    const int c0 = (int)(unit % per) * 8;
-    const bool rows = c0 < p.seg_r;
-    const int col = rows ? c0 : c0 - p.seg_r;
-    const int n = rows ? p.N_r : p.N_c;
-    const float *src = (rows ? p.p_r : p.p_c) + t * n + col;
-    float v[8];
-    const bool keep = !p.mask || p.mask[t];
+// 8 log-probabilities from column col on (those past n: none), as fast as the
+// row's alignment allows.
+__device__ __forceinline__ void load_logp8(const float *row, int col, int n, bool vec, float *v) {
+    if (vec && col + 8 <= n) {
+        const float4 a = reinterpret_cast<const float4 *>(row + col)[0];
+        const float4 b = reinterpret_cast<const float4 *>(row + col)[1];
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = keep && col + i < n ? kScaleP * expf(src[i]) : 0.f;
+        for (int i = 0; i < 8; ++i) v[i] = col + i < n ? row[col + i] : -INFINITY;
+    }
+}
+__device__ __forceinline__ bool float4_rows(const float *p, int n) {
+    return (n & 3) == 0 && (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
+}
+
+// A warp's 256 columns of a row of P: both segments, the padding as zeros.
+__device__ __forceinline__ void prep_probs(const BalPrep &p, int64_t t, int c0, bool vec_r, bool vec_c) {
+    c0 += 8 * (int)lane_id();
+    if (c0 >= p.ld) return;
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (!p.mask || p.mask[t]) {
+        const bool rows = c0 < p.seg_r;
+        load_logp8(rows ? p.p_r + t * p.N_r : p.p_c + t * p.N_c, rows ? c0 : c0 - p.seg_r,
+                   rows ? p.N_r : p.N_c, rows ? vec_r : vec_c, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = kScaleP * expf(v[i]);
+    }
     uint4 hi, lo;
     split8_f16(v, &hi, &lo);
     *reinterpret_cast<uint4 *>(p.P_hi + t * p.ld + c0) = hi;
     *reinterpret_cast<uint4 *>(p.P_lo + t * p.ld + c0) = lo;
 }
 
-constexpr int kPrepThreads = 256;
+// The pieces (row, part) that a warp takes, `warps` apart in row-major order.
+struct Pieces {
+    int64_t row, drow;
+    int part, dpart, parts;
+    __device__ Pieces(int64_t first, int64_t warps, int n) : parts(n) {
+        row = first / n;
+        part = (int)(first % n);
+        drow = warps / n;
+        dpart = (int)(warps % n);
+    }
+    __device__ void next() {
+        row += drow;
+        part += dpart;
+        if (part >= parts) {
+            part -= parts;
+            ++row;
+        }
+    }
+};
 
-// Work units of a CTA: first the 32 x 32 tiles of the counts (F and its
-// transpose, padded with zeros), then 8-value pieces of P, then of x.
-__global__ void __launch_bounds__(kPrepThreads) balance_prep_kernel(const BalPrep p) {
-    __shared__ float tile[32][33];
+constexpr int kPrepThreads = 256, kPrepPerSm = 8;     // all of the grid resident: 32 registers
+
+// Largest finite magnitude of 8 bf16 values, as fp32 bits.
+__device__ __forceinline__ uint32_t top8(const uint4 &u) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t a = (w[i] << 16) & 0x7fff0000u, b = w[i] & 0x7fff0000u;
+        if (a < 0x7f800000u) m = max(m, a);
+        if (b < 0x7f800000u) m = max(m, b);
+    }
+    return m;
+}
+// ... of a warp's 1024 columns of a row of d8 vectors, four loads at a time
+__device__ __forceinline__ uint32_t top_row(const uint16_t *row, int part, int d8) {
+    uint4 u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int c = part * 128 + 32 * i + (int)lane_id();
+        u[i] = c < d8 ? reinterpret_cast<const uint4 *>(row)[c] : make_uint4(0, 0, 0, 0);
+    }
+    return max(max(top8(u[0]), top8(u[1])), max(top8(u[2]), top8(u[3])));
+}
+
+// Largest value of the CTA's threads into *out, with an atomic only where it is
+// larger than what is there: atomics on one address take 2 to 4 ns each, one
+// after another, so one per warp (9472 of them) cost more than the reading.
+template <typename T>
+__device__ __forceinline__ void cta_max(T m, T *out) {
+    __shared__ T best;
+    __syncthreads();
+    if (threadIdx.x == 0) best = 0;
+    __syncthreads();
+    m = __reduce_max_sync(0xffffffffu, m);
+    if (m && lane_id() == 0) atomicMax(&best, m);
+    __syncthreads();
+    if (threadIdx.x == 0 && best > *reinterpret_cast<volatile T *>(out)) atomicMax(out, best);
+}
+
+// Two values at `at` as hi and lo.
+__device__ __forceinline__ void store_pair(uint16_t *hi, uint16_t *lo, int64_t at, float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    const float2 f = __half22float2(h);
+    *reinterpret_cast<__half2 *>(hi + at) = h;
+    *reinterpret_cast<__half2 *>(lo + at) = __floats2half2_rn(a - f.x, b - f.y);
+}
+
+// Work of a CTA: the 64 x 64 tiles of the counts (F and its transpose, padded
+// with zeros), then rows of P and the magnitudes of x and W.
+__global__ void __launch_bounds__(kPrepThreads, kPrepPerSm) balance_prep_kernel(const BalPrep p) {
+    __shared__ float tile[64][65];
     grid_dependency_wait();
     grid_dependents_launch();
-    const int tr = p.pr / 32, tc = p.pc / 32;
-    bool big = false;
+    const int tr = p.pr / 64, tc = p.pc / 64;
+    const bool even = (p.N_c & 1) == 0 && (reinterpret_cast<uintptr_t>(p.counts) & 7u) == 0;
+    int most = 0;
     for (int u = blockIdx.x; u < tr * tc; u += gridDim.x) {
-        const int i0 = (u / tc) * 32, j0 = (u % tc) * 32;
-        const int a = (int)threadIdx.x >> 5, l = (int)threadIdx.x & 31;
-        __syncthreads();
-        for (int r = a; r < 32; r += 8) {
-            const int i = i0 + r, j = j0 + l;
-            const int c = i < p.N_r && j < p.N_c ? p.counts[(int64_t)i * p.N_c + j] : 0;
-            big |= c > kExactCount;
-            const float f = (float)c * kScaleF;
-            tile[r][l] = f;
+        const int i0 = (u / tc) * 64, j0 = (u % tc) * 64;
+        const int a = (int)threadIdx.x >> 5, l2 = 2 * ((int)threadIdx.x & 31);
+        int2 c[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int i = i0 + a + 8 * k, j = j0 + l2;
+            const int32_t *src = p.counts + (int64_t)i * p.N_c + j;
+            c[k] = make_int2(0, 0);
             if (i < p.N_r) {
-                p.F_hi[(int64_t)i * p.pc + j] = f16_bits(f);
-                p.F_lo[(int64_t)i * p.pc + j] = f16_bits(f - f16_of(f));
+                if (even && j < p.N_c) c[k] = *reinterpret_cast<const int2 *>(src);
+                if (!even && j < p.N_c) c[k].x = src[0];
+                if (!even && j + 1 < p.N_c) c[k].y = src[1];
             }
         }
+        __syncthreads();                             // the tile is free again
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int r = a + 8 * k, i = i0 + r;
+            most = max(most, max(c[k].x, c[k].y));
+            const float f[2] = {(float)c[k].x * kScaleF, (float)c[k].y * kScaleF};
+            tile[r][l2] = f[0];
+            tile[r][l2 + 1] = f[1];
+            if (i < p.N_r) store_pair(p.F_hi, p.F_lo, (int64_t)i * p.pc + j0 + l2, f[0], f[1]);
+        }
+        __syncthreads();
         if (p.T_hi) {
-            __syncthreads();
-            for (int r = a; r < 32; r += 8) {
-                const int j = j0 + r, i = i0 + l;
-                const float f = tile[l][r];
-                if (j < p.N_c) {
-                    p.T_hi[(int64_t)j * p.pr + i] = f16_bits(f);
-                    p.T_lo[(int64_t)j * p.pr + i] = f16_bits(f - f16_of(f));
-                }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int r = a + 8 * k, j = j0 + r;
+                if (j < p.N_c)
+                    store_pair(p.T_hi, p.T_lo, (int64_t)j * p.pr + i0 + l2, tile[l2][r], tile[l2 + 1][r]);
             }
         }
     }
-    if (__syncthreads_or(big) && threadIdx.x == 0) atomicOr(p.big, 1);
+    cta_max(most, &p.hdr->most);
 
-    const int64_t step = (int64_t)gridDim.x * kPrepThreads;
-    const int64_t at = (int64_t)blockIdx.x * kPrepThreads + threadIdx.x;
-    const int64_t units = (int64_t)p.L * (p.ld >> 3);
-    for (int64_t u = at; u < units; u += step) prep_probs(p, u);
-    if (p.xs) {
-        const int64_t n = (int64_t)p.L * (p.d >> 3);
-        for (int64_t u = at; u < n; u += step) {
-            const int64_t t = u / (p.d >> 3);
-            reinterpret_cast<uint4 *>(p.xs)[u] =
-                p.mask[t] ? reinterpret_cast<const uint4 *>(p.x)[u] : make_uint4(0, 0, 0, 0);
+    // one warp per 256 columns of a row from here on
+    const int64_t warps = (int64_t)gridDim.x * (kPrepThreads / 32);
+    const int64_t w0 = (int64_t)blockIdx.x * (kPrepThreads / 32) + (threadIdx.x >> 5);
+    const bool vec_r = float4_rows(p.p_r, p.N_r), vec_c = float4_rows(p.p_c, p.N_c);
+    for (Pieces u(w0, warps, (p.ld + 255) / 256); u.row < p.L; u.next())
+        prep_probs(p, u.row, u.part * 256, vec_r, vec_c);
+    if (p.x) {
+        const int d8 = p.d >> 3, dp = (d8 + 127) / 128;
+        uint32_t top = 0;
+        for (Pieces u(w0, warps, dp); u.row < p.L; u.next())
+            if (!p.mask || p.mask[u.row]) top = max(top, top_row(p.x + u.row * p.d, u.part, d8));
+        cta_max(top, &p.hdr->x_top);
+        top = 0;
+        for (Pieces u(w0, warps, dp); u.row < p.N_r + p.N_c; u.next())
+            top = max(top, top_row(u.row < p.N_r ? p.W_r + u.row * p.d
+                                                 : p.W_c + (u.row - p.N_r) * p.d, u.part, d8));
+        cta_max(top, &p.hdr->w_top);
+    }
+    if (!p.mask) {
+        if (blockIdx.x == 0 && threadIdx.x == 0) p.hdr->kept = p.L;
+    } else {
+        // a few CTAs count, with one atomic each
+        int kept = 0;
+        for (int64_t t = (int64_t)blockIdx.x * kCountSpan; t < p.L; t += (int64_t)gridDim.x * kCountSpan)
+            for (int i = (int)threadIdx.x; i < kCountSpan && t + i < p.L; i += kPrepThreads)
+                kept += p.mask[t + i] != 0;
+        kept = warp_isum(kept);
+        if (kept && lane_id() == 0) atomicAdd(&p.hdr->kept, kept);
+    }
+}
+
+// x and W in fp16, scaled: masked rows of x as zeros (what they hold must not
+// meet a zero gradient as NaN), W_r and W_c one under the other with zero rows
+// between, as the columns of ds lie.
+struct BalCast {
+    const uint16_t *x, *W_r, *W_c;
+    const uint8_t *mask;
+    int L, N_r, N_c, d, pr, ld;
+    uint16_t *x16, *w16;
+    const BalHeader *hdr;
+};
+__global__ void __launch_bounds__(kPrepThreads) balance_cast_kernel(const BalCast p) {
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const float sx = pow2f(top_exp(p.hdr->x_top)), sw = pow2f(top_exp(p.hdr->w_top));
+    const int d8 = p.d >> 3;
+    const int64_t warps = (int64_t)gridDim.x * (kPrepThreads / 32);
+    for (int64_t row = (int64_t)blockIdx.x * (kPrepThreads / 32) + (threadIdx.x >> 5);
+         row < (int64_t)p.L + p.ld; row += warps) {
+        const bool w = row >= p.L;
+        const int64_t r = w ? row - p.L : row;
+        const uint16_t *src = nullptr;
+        if (!w) {
+            if (!p.mask || p.mask[r]) src = p.x + r * p.d;
+        } else if (r < p.pr) {
+            if (r < p.N_r) src = p.W_r + r * p.d;
+        } else if (r - p.pr < p.N_c) {
+            src = p.W_c + (r - p.pr) * p.d;
+        }
+        uint4 *dst = reinterpret_cast<uint4 *>((w ? p.w16 : p.x16) + r * p.d);
+        const float s = w ? sw : sx;
+        for (int c = (int)lane_id(); c < d8; c += 32) {
+            uint4 o = make_uint4(0, 0, 0, 0);
+            if (src) {
+                const uint4 in = reinterpret_cast<const uint4 *>(src)[c];
+                const uint32_t a[4] = {in.x, in.y, in.z, in.w};
+                uint32_t h[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const __half2 b = __floats2half2_rn(__uint_as_float(a[i] << 16) * s,
+                                                        __uint_as_float(a[i] & 0xffff0000u) * s);
+                    h[i] = *reinterpret_cast<const uint32_t *>(&b);
+                }
+                o = make_uint4(h[0], h[1], h[2], h[3]);
+            }
+            dst[c] = o;
         }
     }
-    int kept = 0;
-    for (int64_t t = at; t < p.L; t += step) kept += !p.mask || p.mask[t];
-    kept = warp_isum(kept);
-    if (kept && lane_id() == 0) atomicAdd(p.n_local, kept);
 }
 
 // -------------------------------------------------------------- tile GEMM
-// C[M, N] = (A_hi + A_lo) B over a K axis of 64-element steps, tiles of 128 x
-// bn.  An operand is K-major (its K axis contiguous in memory) or MN-major
-// (its M or N axis contiguous); either way a TMA box is 64 elements (128
-// bytes, one swizzle atom) wide along the contiguous axis.
-constexpr int BM = 128, BN = 256, BK = kSwK, STAGES = 3;
+// C[M, N] = (A_hi + A_lo) B over a K axis of 64-element steps, tiles of 256 x
+// bn, each computed by a pair of CTAs (a cluster of 2, cta_group::2): CTA r
+// holds rows 128 r .. + 127 of A (hi and lo) and half of the B tile in its
+// shared memory, the pair's first CTA issues the MMAs, and each CTA's TMEM
+// receives its 128 rows of C.  With both halves of A in shared memory a CTA
+// of its own (128 x 256 tiles) would read 96 and fill 64 bytes of it per
+// clock, against 128; the pair's halves of B make that 64 and 47.
+// An operand is K-major (its K axis contiguous in memory: the products with
+// F) or MN-major (its M or N axis contiguous: W and x, and ds as ds^T); either
+// way a TMA box is 64 elements (128 bytes, one swizzle atom) wide along the
+// contiguous axis.
+constexpr int BM = 128, BN = 256, BK = kSwK, STAGES = 4;     // BM: rows of one CTA
 constexpr int kBytesA = BM * BK * 2;             // 16 KB, each of hi and lo
-constexpr int kBytesB = BN * BK * 2;             // 32 KB at most
+constexpr int kBytesB = BN / 2 * BK * 2;         // 16 KB at most: half of the B tile
 constexpr int kBlockMN = 64 * BK * 2;            // an MN-major box: 64 K rows of 128 bytes
 constexpr uint32_t kTmemCols = 2 * BN;
-constexpr int kEpiWarps = 8;
+constexpr int kEpiWarps = 8;                     // two per TMEM lane quarter
 constexpr int kEpiBlocks = BN / 64;              // 32-column blocks of a tile for one of them
 constexpr int kThreads = 32 * (2 + kEpiWarps);
-constexpr uint32_t kIdescBf16 = umma_idesc_bf16(BM, 0);        // the tile width is added per problem
-constexpr uint32_t kIdescF16 = kIdescBf16 & ~((1u << 7) | (1u << 10));   // A and B fp16 (formats 0)
-constexpr int kMaxProbs = 3, kMaxMaps = 9;
+constexpr uint32_t kIdescF16 =                   // A and B fp16 (formats 0); the width is added
+    umma_idesc_bf16(2 * BM, 0) & ~((1u << 7) | (1u << 10));
+constexpr int kMaxProbs = 2, kMaxMaps = 6;
 // K steps that are summed in TMEM before the epilogue warps add them to their
 // registers.  The tensor core cuts off what falls below its accumulator at
 // every instruction (8 of them in a step), always towards zero: over the 512
@@ -232,57 +402,62 @@ constexpr int kChunk = 4;
 struct __align__(1024) GemmSmem {
     uint8_t a[STAGES][2 * kBytesA];
     uint8_t b[STAGES][kBytesB];
-    uint64_t full[STAGES];
+    float turn[kEpiWarps][32 * 32];              // an epilogue warp's 32 x 32 block, between its layouts
+    uint64_t full[STAGES];                       // used in the pair's first CTA
     uint64_t empty[STAGES];
-    uint64_t tfull[2];
-    uint64_t tempty[2];
+    uint64_t tfull[2];                           // accumulator ready for the epilogue
+    uint64_t tempty[2];                          // accumulator drained (first CTA: both CTAs' warps)
     uint32_t tmem_base;
     int abort;
 };
 
 struct GemmProb {
     int M, N;                     // rows and columns of C
-    int bn, tiles_n, tiles;       // tile width (a multiple of 32), tiles in N, tiles in all
+    int bn, tiles_n, tiles;       // tile width, tiles in N, tiles in all
     int nk;                       // 64-element steps of the K axis
     int a_hi, a_lo;               // tensor maps of A
     int a_c0;                     // first column of A's segment in its matrix
-    int b, b2;                    // maps of B; b2: the remainder F_lo, or B past step nk1
-    int nk1;                      // MN-major B: steps taken from b (the rest from b2)
-    float *out;                   // C in fp32 (products with W and x)
-    int ld_out, accumulate;
-    const float *p;               // log-probabilities beside this C (products with F)
+    int b, b_lo;                  // maps of B, and of the remainder F_lo
+    const float *p;               // forward: log-probabilities beside this C
+    const uint16_t *P_hi, *P_lo;  // backward: P beside this C, column 0 of its segment
     uint16_t *ds_hi, *ds_lo;      // their gradient, column 0 of this segment
     int seg;                      // columns of the segment (N padded to 64; the pad gets zeros)
+    float *out, *out2;            // C in fp32: rows below `split`, and from `split` on
+    int split, rows1, rows2;      // rows of out and of out2 (the others are padding)
+    int accumulate;
 };
 
 struct GemmArgs {
-    GemmProb prob[kMaxProbs];
+    GemmProb prob[kMaxProbs];     // gradients: dW (A is ds^T), then dx
     int nprob, tiles;
-    const int *big;               // counts above kExactCount: also multiply by F_lo
+    int ld;                       // columns of ds
     const uint8_t *mask;
     float *part;                  // forward: sums over a tile's columns [tiles_n * 2, L]
     const float *token_loss;      // backward
-    const int32_t *n_tokens, *n_local;
+    const int32_t *n_tokens;
     float factor;                 // dloss N / K
-    int *status;
+    BalHeader *hdr;
 };
 struct GemmMaps { CUtensorMap m[kMaxMaps]; };
 
-// what a launch computes: U with the forward's sums; U and V with ds; dx, dW_r, dW_c
+// what a launch computes: U with the forward's sums; U and V with ds; dW and dx
 enum : int { kFwd = 0, kGrid = 1, kGrads = 2 };
 
-// Tiles are dealt out back and forth over the CTAs, longest first, so that
-// the CTAs with a long first tile get the last of the short ones.
+// Tiles are dealt out back and forth over the pairs, longest first, so that
+// the pairs with a long first tile get the last of the short ones.
 __device__ __forceinline__ int tile_of(int turn, int tiles) {
-    const int c = (turn & 1) ? (int)(gridDim.x - 1 - blockIdx.x) : (int)blockIdx.x;
-    const int64_t i = (int64_t)turn * gridDim.x + c;
+    const int pairs = (int)(gridDim.x >> 1), pair = (int)(blockIdx.x >> 1);
+    const int64_t i = (int64_t)turn * pairs + ((turn & 1) ? pairs - 1 - pair : pair);
     return i < tiles ? (int)i : -1;
+}
+__device__ __forceinline__ bool turns_left(int turn, int tiles) {
+    return (int64_t)turn * (gridDim.x >> 1) < tiles;
 }
 
 __device__ __forceinline__ int find_prob(const GemmArgs &g, int *tile) {
-    int k = 0;
-    while (k + 1 < g.nprob && *tile >= g.prob[k].tiles) *tile -= g.prob[k++].tiles;
-    return k;
+    if (g.nprob == 1 || *tile < g.prob[0].tiles) return 0;
+    *tile -= g.prob[0].tiles;
+    return 1;
 }
 
 // Descriptor of an MN-major tile: 64-element blocks of the M or N axis
@@ -298,15 +473,32 @@ __device__ __forceinline__ int steps_of(const GemmProb &p, bool big) {
     return MODE != kGrads && big ? 2 * p.nk : p.nk;
 }
 
+// Arrive on the pair's first CTA's barrier.  What it orders are TMEM reads,
+// which have completed; at cluster scope (and with acquires at cluster scope
+// on the other side) each arrive would also wait for the warp's global stores,
+// and each wait drop the SM's L1.
+__device__ __forceinline__ void mbar_arrive_pair(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void prefetch_l2(const void *at) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+}
+
+// Word of element (r, c) of a warp's 32 x 32 block: rows and columns are both
+// read and written without bank conflicts.
+__device__ __forceinline__ int turned(int r, int c) { return r * 32 + (c ^ r); }
+
 template <int MODE>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 balance_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ GemmArgs g) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
     GemmSmem &sm = *reinterpret_cast<GemmSmem *>(smem_raw + pad);
     const int warp = threadIdx.x >> 5;
     const unsigned lane = lane_id();
-    int *status = g.status;
+    const uint32_t rank = cluster_ctarank();         // 0: issues the MMAs
+    int *status = &g.hdr->status;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -315,38 +507,38 @@ balance_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&sm.tfull[b], 1);
-            mbar_init(&sm.tempty[b], kEpiWarps);
+            mbar_init(&sm.tempty[b], 2 * kEpiWarps);
         }
         sm.abort = 0;
         fence_barrier_init();
     }
     if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
                      ::"r"(smem_u32(&sm.tmem_base)), "r"(kTmemCols));
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
     }
     tc_fence_before();
     __syncthreads();
+    cluster_sync();                                  // both CTAs' barriers exist
     tc_fence_after();
     const uint32_t tmem = sm.tmem_base;
     grid_dependency_wait();
     grid_dependents_launch();
-    const bool big = MODE != kGrads && *g.big != 0;
-
+    const bool big = MODE != kGrads && g.hdr->most > kExactCount;
 
     if (warp == 0) {
         if (lane == 0) {
-            // ---- TMA producer
+            // ---- TMA producer (both CTAs): completion counted on the first CTA's barrier
             int it = 0, issued_from = 0;
-            for (int turn = 0; !sm.abort; ++turn) {
+            for (int turn = 0; !sm.abort && turns_left(turn, g.tiles); ++turn) {
                 int tile = tile_of(turn, g.tiles);
-                if ((int64_t)turn * gridDim.x >= g.tiles) break;
                 if (tile < 0) continue;
                 const int pk = find_prob(g, &tile);
                 const GemmProb &p = g.prob[pk];
-                const int m0 = (tile / p.tiles_n) * BM, n0 = (tile % p.tiles_n) * p.bn;
+                const int m0 = (tile / p.tiles_n) * 2 * BM + (int)rank * BM;
+                const int n0 = (tile % p.tiles_n) * p.bn + (int)rank * (p.bn / 2);
                 const int steps = steps_of<MODE>(p, big);
-                const bool a_mn = MODE == kGrads && pk < g.nprob - 1;   // dW: A is ds^T
+                const bool a_mn = MODE == kGrads && pk == 0;             // dW: A is ds^T
                 for (int st = 0; st < steps; ++st, ++it) {
                     const int s = it % STAGES;
                     if (it >= STAGES &&
@@ -356,56 +548,54 @@ balance_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant
                     }
                     const bool rest = MODE != kGrads && st >= p.nk;      // hi times F_lo
                     const int kb = rest ? st - p.nk : st;
-                    mbar_arrive_expect_tx(&sm.full[s],
-                                          (uint32_t)((rest ? 1 : 2) * kBytesA + p.bn * BK * 2));
+                    if (rank == 0)
+                        mbar_arrive_expect_tx(&sm.full[s],
+                                              (uint32_t)(2 * (rest ? 1 : 2) * kBytesA + p.bn * BK * 2));
+                    const uint32_t fb = smem_in_cta(&sm.full[s], 0);
                     uint8_t *a = sm.a[s], *b = sm.b[s];
                     if (a_mn) {
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            tma_load_2d(a + i * kBlockMN, &maps.m[p.a_hi], p.a_c0 + m0 + 64 * i,
-                                        kb * BK, &sm.full[s]);
-                            tma_load_2d(a + kBytesA + i * kBlockMN, &maps.m[p.a_lo],
-                                        p.a_c0 + m0 + 64 * i, kb * BK, &sm.full[s]);
+                            tma_load_2d_pair(a + i * kBlockMN, &maps.m[p.a_hi], m0 + 64 * i, kb * BK, fb);
+                            tma_load_2d_pair(a + kBytesA + i * kBlockMN, &maps.m[p.a_lo], m0 + 64 * i,
+                                             kb * BK, fb);
                         }
                     } else {
-                        tma_load_2d(a, &maps.m[p.a_hi], p.a_c0 + kb * BK, m0, &sm.full[s]);
+                        tma_load_2d_pair(a, &maps.m[p.a_hi], p.a_c0 + kb * BK, m0, fb);
                         if (!rest)
-                            tma_load_2d(a + kBytesA, &maps.m[p.a_lo], p.a_c0 + kb * BK, m0,
-                                        &sm.full[s]);
+                            tma_load_2d_pair(a + kBytesA, &maps.m[p.a_lo], p.a_c0 + kb * BK, m0, fb);
                     }
                     if (MODE == kGrads) {
-                        const bool second = kb >= p.nk1;
-                        const CUtensorMap *tm = &maps.m[second ? p.b2 : p.b];
-                        const int k0 = (second ? kb - p.nk1 : kb) * BK;
-                        for (int j = 0; j < p.bn / 64; ++j)
-                            tma_load_2d(b + j * kBlockMN, tm, n0 + 64 * j, k0, &sm.full[s]);
+                        for (int j = 0; j < p.bn / 128; ++j)
+                            tma_load_2d_pair(b + j * kBlockMN, &maps.m[p.b], n0 + 64 * j, kb * BK, fb);
                     } else {
-                        tma_load_2d(b, &maps.m[rest ? p.b2 : p.b], kb * BK, n0, &sm.full[s]);
+                        tma_load_2d_pair(b, &maps.m[rest ? p.b_lo : p.b], kb * BK, n0, fb);
                     }
                     issued_from = it + 1 > STAGES ? it + 1 - STAGES : 0;
                 }
             }
-            if (sm.abort)
+            if (sm.abort && rank == 0) {
+                // let the loads already issued land before the CTA can exit
                 for (int k = issued_from; k < it; ++k)
                     mbar_wait(&sm.full[k % STAGES], (uint32_t)((k / STAGES) & 1), status);
+            }
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0) {
-            // ---- MMA issuer
+        if (lane == 0 && rank == 0) {
+            // ---- MMA issuer (the pair's first CTA)
             int it = 0, lt = 0;
             bool ok = true;
-            for (int turn = 0; ok; ++turn) {
+            for (int turn = 0; ok && turns_left(turn, g.tiles); ++turn) {
                 int tile = tile_of(turn, g.tiles);
-                if ((int64_t)turn * gridDim.x >= g.tiles) break;
                 if (tile < 0) continue;
                 const int pk = find_prob(g, &tile);
                 const GemmProb &p = g.prob[pk];
                 const int steps = steps_of<MODE>(p, big);
-                const bool a_mn = MODE == kGrads && pk < g.nprob - 1;
+                const bool a_mn = MODE == kGrads && pk == 0;
                 // bits 15 and 16 of the instruction descriptor: A, B are MN-major
-                const uint32_t idesc = (MODE == kGrads ? kIdescBf16 | 1u << 16 : kIdescF16) |
-                                       ((uint32_t)(p.bn >> 3) << 17) | (a_mn ? 1u << 15 : 0u);
+                const uint32_t idesc = kIdescF16 | ((uint32_t)(p.bn >> 3) << 17) |
+                                       (a_mn ? 1u << 15 : 0u) | (MODE == kGrads ? 1u << 16 : 0u);
                 // a 16-deep slice: 32 bytes along a K-major atom, or 16 K rows
                 const uint64_t a_step = (a_mn ? 16 * 128 : 32) >> 4;
                 const uint64_t b_step = (MODE == kGrads ? 16 * 128 : 32) >> 4;
@@ -414,8 +604,8 @@ balance_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant
                     const int s = it % STAGES;
                     const bool first = st % kChunk == 0;
                     if (first) {                              // the next accumulator
-                        if (lt >= 2 &&
-                            !mbar_wait(&sm.tempty[lt & 1], (uint32_t)(((lt >> 1) - 1) & 1), status)) {
+                        if (lt >= 2 && !mbar_wait(&sm.tempty[lt & 1],
+                                                          (uint32_t)(((lt >> 1) - 1) & 1), status)) {
                             ok = false;
                             break;
                         }
@@ -428,20 +618,19 @@ balance_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant
                     tc_fence_after();
                     const uint64_t ah = a_mn ? sw128_desc_mn(sm.a[s]) : sw128_desc(sm.a[s]);
                     const uint64_t bd = MODE == kGrads ? sw128_desc_mn(sm.b[s]) : sw128_desc(sm.b[s]);
-                    const bool rest = MODE != kGrads && st >= p.nk;
 #pragma unroll
                     for (int k = 0; k < BK / 16; ++k)
-                        umma_bf16(acc, ah + k * a_step, bd + k * b_step, idesc,
-                                  (!first || k > 0) ? 1u : 0u);
-                    if (!rest) {
+                        umma_bf16_pair(acc, ah + k * a_step, bd + k * b_step, idesc,
+                                       (!first || k > 0) ? 1u : 0u);
+                    if (MODE == kGrads || st < p.nk) {
                         const uint64_t al = ah + (kBytesA >> 4);
 #pragma unroll
                         for (int k = 0; k < BK / 16; ++k)
-                            umma_bf16(acc, al + k * a_step, bd + k * b_step, idesc, 1u);
+                            umma_bf16_pair(acc, al + k * a_step, bd + k * b_step, idesc, 1u);
                     }
-                    umma_commit(&sm.empty[s]);
+                    umma_commit_pair(&sm.empty[s]);           // frees stage s in both CTAs
                     if (st % kChunk == kChunk - 1 || st == steps - 1) {
-                        umma_commit(&sm.tfull[lt & 1]);
+                        umma_commit_pair(&sm.tfull[lt & 1]);  // both CTAs' epilogues may read
                         ++lt;
                     }
                 }
@@ -450,31 +639,57 @@ balance_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant
         }
         __syncwarp();
     } else {
-        // ---- epilogue: warp w reads TMEM lanes 32*(w % 4) .. +31 (tile rows)
-        // and every second block of 32 columns
+        // ---- epilogue: warp w reads TMEM lanes 32*(w % 4) .. +31 (this CTA's
+        // rows of the tile) and every second block of 32 columns
         const int quarter = warp & 3;
         const int half = (warp - 2) >> 2;
-        float c = 0.f;
-        if (MODE == kGrid) {
-            const int n = *g.n_tokens, nl = *g.n_local;
-            c = n > 0 && nl > 0 ? g.factor / (float)n / (float)nl : 0.f;
+        const uint32_t tempty0 = smem_in_cta(&sm.tempty[0], 0);
+        const uint32_t tempty1 = smem_in_cta(&sm.tempty[1], 0);
+        float *turn_buf = sm.turn[warp - 2];
+        float scale1 = 1.f, scale2 = 1.f;            // dW, dx: the scales that come out again
+        if (MODE == kGrid) scale1 = pow2f(1 - count_exp(g.hdr->most));   // 2^15, and P's 2^-14
+        if (MODE == kGrads) {
+            const int n = *g.n_tokens, kept = g.hdr->kept;
+            scale1 = n > 0 && kept > 0 ? g.factor / (float)n / (float)kept *
+                                             pow2f(count_exp(g.hdr->most) - 15) : 0.f;
         }
         int lt = 0;
         bool ok = true;
-        for (int turn = 0; ok; ++turn) {
+        for (int turn = 0; ok && turns_left(turn, g.tiles); ++turn) {
             int tile = tile_of(turn, g.tiles);
-            if ((int64_t)turn * gridDim.x >= g.tiles) break;
             if (tile < 0) continue;
-            const GemmProb &p = g.prob[find_prob(g, &tile)];
-            const int m0 = (tile / p.tiles_n) * BM, tn = tile % p.tiles_n, n0 = tn * p.bn;
+            const int pk = find_prob(g, &tile);
+            const GemmProb &p = g.prob[pk];
+            const int row0 = (tile / p.tiles_n) * 2 * BM + (int)rank * BM + quarter * 32;
+            const int tn = tile % p.tiles_n, n0 = tn * p.bn;
             const int steps = steps_of<MODE>(p, big), blocks = p.bn / 32;
+            const int row = row0 + (int)lane;
+            // what the tile's end will read of this lane's row is asked of L2 now
+            if (row < p.M) {
+                for (int q = half; q < blocks; q += 2) {
+                    const int col = n0 + 32 * q;
+                    if (MODE == kFwd && col < p.N) prefetch_l2(p.p + (int64_t)row * p.N + col);
+                    if (MODE == kGrid && col < p.seg) {
+                        prefetch_l2(p.P_hi + (int64_t)row * g.ld + col);
+                        prefetch_l2(p.P_lo + (int64_t)row * g.ld + col);
+                    }
+                    if (MODE == kGrads && p.accumulate && col < p.N) {
+                        const bool second = row >= p.split;
+                        const int m = second ? row - p.split : row;
+                        if (m < (second ? p.rows2 : p.rows1))
+                            prefetch_l2((second ? p.out2 : p.out) + (int64_t)m * p.N + col);
+                    }
+                }
+            }
             float sum[kEpiBlocks][32];
 #pragma unroll
             for (int q = 0; q < kEpiBlocks; ++q)
 #pragma unroll
                 for (int j = 0; j < 32; ++j) sum[q][j] = 0.f;
             for (int st = 0; st < steps; st += kChunk, ++lt) {
-                if (!mbar_wait(&sm.tfull[lt & 1], (uint32_t)((lt >> 1) & 1), status)) {
+                // the warp gives up as one: its lanes meet again below
+                const bool got = mbar_wait(&sm.tfull[lt & 1], (uint32_t)((lt >> 1) & 1), status);
+                if (!__all_sync(0xffffffffu, got)) {
                     ok = false;
                     break;
                 }
@@ -492,74 +707,129 @@ balance_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant
                         }
                     }
                 }
-                // this accumulator may be overwritten once every epilogue warp is done
+                // this accumulator may be overwritten once every epilogue warp of
+                // both CTAs is done (the first CTA's barrier counts all 16)
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.tempty[lt & 1]);
+                if (lane == 0) mbar_arrive_pair((lt & 1) ? tempty1 : tempty0);
             }
             if (!ok) break;
-            const int row = m0 + quarter * 32 + (int)lane;
-            const bool in = row < p.M;
-            const bool keep = MODE != kGrads && in && (!g.mask || g.mask[row]);
-            const float lt_loss = MODE == kGrid && keep ? g.token_loss[row] : 0.f;
+            // a masked row has P = 0, its sums are finite and its token_loss is not used
+            const bool keep = MODE != kGrads && row < p.M && (!g.mask || g.mask[row]);
+            const bool vec = MODE == kFwd && float4_rows(p.p, p.N);
+            const float l_t = MODE == kGrid && keep ? g.token_loss[row] : 0.f;
+            if (MODE == kGrads) scale2 = pow2f(-top_exp(pk == 0 ? g.hdr->x_top : g.hdr->w_top));
             float part = 0.f;
 #pragma unroll
             for (int q = 0; q < kEpiBlocks; ++q) {
-                if (half + 2 * q >= blocks) continue;
-                const float (&r)[32] = sum[q];
-                const int col = n0 + 32 * (half + 2 * q);
-                if (MODE == kFwd) {
+                const int col0 = n0 + 32 * (half + 2 * q);
+                if (half + 2 * q >= blocks || col0 >= (MODE == kGrid ? p.seg : p.N)) break;
+                if constexpr (MODE == kFwd) {
+                    // each lane its own row: the sums stay where they are (no lane
+                    // waits for another in here)
                     if (keep) {
-                        const float *src = p.p + (int64_t)row * p.N + col;
+                        const float *src = p.p + (int64_t)row * p.N;
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (col + j < p.N) part = fmaf(expf(src[j]), kUnscale * r[j], part);
-                    }
-                } else if (MODE == kGrid) {
-                    if (in && col < p.seg) {
-                        const float *src = p.p + (int64_t)row * p.N + col;
-#pragma unroll
-                        for (int o = 0; o < 4; ++o) {
+                        for (int j = 0; j < 32; j += 8) {
                             float v[8];
+                            load_logp8(src, col0 + j, p.N, vec, v);
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                const int k = 8 * o + j;
-                                v[j] = keep && col + k < p.N
-                                           ? c * expf(src[k]) * (kUnscale * r[k] - lt_loss) : 0.f;
-                            }
-                            uint4 hi, lo;
-                            split8(v, &hi, &lo);
-                            const int64_t at = (int64_t)row * p.ld_out + col + 8 * o;
-                            *reinterpret_cast<uint4 *>(p.ds_hi + at) = hi;
-                            *reinterpret_cast<uint4 *>(p.ds_lo + at) = lo;
+                            for (int k = 0; k < 8; ++k) part = fmaf(expf(v[k]), sum[q][j + k], part);
                         }
                     }
-                } else if (in) {
-                    float4 *dst = reinterpret_cast<float4 *>(p.out + (int64_t)row * p.ld_out + col);
+                } else {
 #pragma unroll
-                    for (int o = 0; o < 8; ++o) {
-                        if (col + 4 * o < p.N) {
-                            float4 v = make_float4(r[4 * o], r[4 * o + 1], r[4 * o + 2], r[4 * o + 3]);
-                            if (p.accumulate) {
-                                const float4 prev = dst[o];
-                                v.x += prev.x;
-                                v.y += prev.y;
-                                v.z += prev.z;
-                                v.w += prev.w;
+                    for (int j = 0; j < 32; ++j) turn_buf[turned((int)lane, j)] = sum[q][j];
+                    __syncwarp();
+                }
+                if constexpr (MODE == kGrid) {
+                    // four rows at a time, four columns to a lane; P as the operand holds it
+                    const int c = 4 * ((int)lane & 7), r0 = (int)lane >> 3;
+                    const int64_t at = (int64_t)(row0 + r0) * g.ld + col0 + c;
+#pragma unroll 1
+                    for (int i4 = 0; i4 < 8; i4 += 4) {
+                        uint2 hi[4], lo[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int64_t o = at + 4 * (i4 + i) * g.ld;
+                            const bool in = row0 + r0 + 4 * (i4 + i) < p.M;
+                            hi[i] = in ? *reinterpret_cast<const uint2 *>(p.P_hi + o) : make_uint2(0, 0);
+                            lo[i] = in ? *reinterpret_cast<const uint2 *>(p.P_lo + o) : make_uint2(0, 0);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int r = r0 + 4 * (i4 + i);
+                            const float l = __shfl_sync(0xffffffffu, l_t, r);
+                            uint32_t oh[2], ol[2];
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const uint32_t wh = k ? hi[i].y : hi[i].x, wl = k ? lo[i].y : lo[i].x;
+                                const float2 ph = __half22float2(*reinterpret_cast<const __half2 *>(&wh));
+                                const float2 pl = __half22float2(*reinterpret_cast<const __half2 *>(&wl));
+                                const float a = (ph.x + pl.x) * scale1 *
+                                                (kUnscale * turn_buf[turned(r, c + 2 * k)] - l);
+                                const float b = (ph.y + pl.y) * scale1 *
+                                                (kUnscale * turn_buf[turned(r, c + 2 * k + 1)] - l);
+                                const __half2 h = __floats2half2_rn(a, b);
+                                const float2 f = __half22float2(h);
+                                const __half2 o = __floats2half2_rn(a - f.x, b - f.y);
+                                oh[k] = *reinterpret_cast<const uint32_t *>(&h);
+                                ol[k] = *reinterpret_cast<const uint32_t *>(&o);
                             }
-                            dst[o] = v;
+                            if (row0 + r < p.M) {
+                                const int64_t o = at + 4 * (i4 + i) * g.ld;
+                                *reinterpret_cast<uint2 *>(p.ds_hi + o) = make_uint2(oh[0], oh[1]);
+                                *reinterpret_cast<uint2 *>(p.ds_lo + o) = make_uint2(ol[0], ol[1]);
+                            }
+                        }
+                    }
+                } else if constexpr (MODE == kGrads) {
+                    // four rows at a time, four columns to a lane
+                    const int c = 4 * ((int)lane & 7), col = col0 + c, r0 = (int)lane >> 3;
+                    // a block lies on one side of the split (both are multiples of 32)
+                    const bool second = row0 >= p.split;
+                    const int m0 = row0 - (second ? p.split : 0) + r0;
+                    const int rows = col < p.N ? (second ? p.rows2 : p.rows1) : 0;
+                    float *out = (second ? p.out2 : p.out) + (int64_t)m0 * p.N + col;
+#pragma unroll 1
+                    for (int i4 = 0; i4 < 8; i4 += 4) {
+                        float4 prev[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            prev[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                            if (p.accumulate && m0 + 4 * (i4 + i) < rows)
+                                prev[i] = *reinterpret_cast<const float4 *>(out + (int64_t)4 * (i4 + i) * p.N);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int r = r0 + 4 * (i4 + i);
+                            float4 v;
+                            v.x = __fmul_rn(turn_buf[turned(r, c)] * scale1, scale2);
+                            v.y = __fmul_rn(turn_buf[turned(r, c + 1)] * scale1, scale2);
+                            v.z = __fmul_rn(turn_buf[turned(r, c + 2)] * scale1, scale2);
+                            v.w = __fmul_rn(turn_buf[turned(r, c + 3)] * scale1, scale2);
+                            if (p.accumulate) {
+                                v.x += prev[i].x;
+                                v.y += prev[i].y;
+                                v.z += prev[i].z;
+                                v.w += prev[i].w;
+                            }
+                            if (m0 + 4 * (i4 + i) < rows)
+                                *reinterpret_cast<float4 *>(out + (int64_t)4 * (i4 + i) * p.N) = v;
                         }
                     }
                 }
+                __syncwarp();
             }
-            if (MODE == kFwd && in) g.part[(int64_t)(2 * tn + half) * p.M + row] = part;
+            if (MODE == kFwd && row < p.M) g.part[(int64_t)(2 * tn + half) * p.M + row] = kUnscale * part;
         }
     }
     tc_fence_before();
     __syncthreads();
+    cluster_sync();                                  // the pair is done with both TMEMs
     if (warp == 1) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;"
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;"
                      ::"r"(tmem), "r"(kTmemCols));
     }
 }
@@ -569,9 +839,8 @@ balance_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant
 constexpr int kLossThreads = 256;
 __global__ void __launch_bounds__(kLossThreads)
 balance_loss_kernel(const float *__restrict__ part, int nparts, int L, float *__restrict__ token_loss,
-                    double *__restrict__ block_sum, int *__restrict__ done, double factor,
-                    const int32_t *__restrict__ n_tokens, const int *__restrict__ n_local,
-                    float *__restrict__ loss) {
+                    double *__restrict__ block_sum, BalHeader *hdr, double factor,
+                    const int32_t *__restrict__ n_tokens, float *__restrict__ loss) {
     __shared__ double sm[kLossThreads / 32];
     __shared__ int last;
     grid_dependency_wait();
@@ -580,6 +849,7 @@ balance_loss_kernel(const float *__restrict__ part, int nparts, int L, float *__
     const int64_t t = (int64_t)blockIdx.x * kLossThreads + threadIdx.x;
     if (t < L) {
         float v = 0.f;
+#pragma unroll 8
         for (int k = 0; k < nparts; ++k) v += part[(int64_t)k * L + t];
         token_loss[t] = v;
         s = v;
@@ -592,7 +862,7 @@ balance_loss_kernel(const float *__restrict__ part, int nparts, int L, float *__
         for (int k = 1; k < kLossThreads / 32; ++k) s += sm[k];
         block_sum[blockIdx.x] = s;
         __threadfence();
-        last = atomicAdd(done, 1) == (int)gridDim.x - 1;
+        last = atomicAdd(&hdr->done, 1) == (int)gridDim.x - 1;
     }
     __syncthreads();
     if (!last) return;
@@ -607,18 +877,38 @@ balance_loss_kernel(const float *__restrict__ part, int nparts, int L, float *__
     __syncthreads();
     if (threadIdx.x == 0) {
         for (int k = 1; k < kLossThreads / 32; ++k) s += sm[k];
-        const double n = *n_tokens, nl = *n_local;
+        const double n = *n_tokens, nl = hdr->kept;
         *loss = n > 0 && nl > 0 ? (float)(factor / (n * nl) * s) : 0.f;
     }
 }
 
 inline int pad64(int n) { return (n + 63) / 64 * 64; }
 
-// tile width: the fewest tiles of at most 256 columns, evened out to `unit`
-inline int tile_width(int n, int unit) {
-    const int tiles = (n + BN - 1) / BN;
-    const int each = (n + tiles - 1) / tiles;
-    return (each + unit - 1) / unit * unit;
+// Width of the tiles of a launch whose problems have n[i] columns and as many
+// 256-row tiles: the one that takes the least time in whole rounds of the
+// pairs.  A K step's 8 MMAs take 4 clocks per column; its shared-memory
+// traffic (operands read and filled) is 64 KB and 192 bytes per column at 128
+// bytes a clock, which is more for narrow tiles.
+int pick_width(const int *n, int probs, int mtiles, int pairs) {
+    int best = 0;
+    int64_t best_cost = 0;
+    for (int bn = BN; bn >= 64; bn -= 32) {
+        int64_t tiles = 0;
+        for (int i = 0; i < probs; ++i) tiles += (int64_t)mtiles * ((n[i] + bn - 1) / bn);
+        const int mma = 4 * bn, smem = 512 + bn * 3 / 2;
+        const int64_t cost = (tiles + pairs - 1) / pairs * (mma > smem ? mma : smem);
+        if (best == 0 || cost < best_cost) {
+            best = bn;
+            best_cost = cost;
+        }
+    }
+    return best;
+}
+
+void set_tiles(GemmProb *p, int cols, int bn) {
+    p->bn = bn;
+    p->tiles_n = (cols + bn - 1) / bn;
+    p->tiles = ((p->M + 2 * BM - 1) / (2 * BM)) * p->tiles_n;
 }
 
 template <int MODE>
@@ -627,18 +917,17 @@ cudaError_t launch_gemm(const GemmMaps &maps, const GemmArgs &g, cudaStream_t st
     const cudaError_t e = cudaFuncSetAttribute(balance_gemm_kernel<MODE>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    const int sms = device_sm_count();
-    return launch(balance_gemm_kernel<MODE>, dim3((unsigned)(g.tiles < sms ? g.tiles : sms)),
-                  dim3(kThreads), (size_t)smem, st, maps, g);
-}
-
-void set_tiles(GemmProb *p, int unit) {
-    p->bn = tile_width(p->N, unit);
-    p->tiles_n = (p->N + p->bn - 1) / p->bn;
-    p->tiles = ((p->M + BM - 1) / BM) * p->tiles_n;
+    const int most = device_sm_count() / 2, pairs = g.tiles < most ? g.tiles : most;
+    return launch(balance_gemm_kernel<MODE>, dim3((unsigned)(2 * pairs)), dim3(kThreads),
+                  (size_t)smem, st, maps, g);
 }
 
 inline size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
+
+inline int fwd_width(int L, int N_r) {
+    const int n[1] = {N_r};
+    return pick_width(n, 1, (L + 2 * BM - 1) / (2 * BM), device_sm_count() / 2);
+}
 
 }  // namespace
 
@@ -658,9 +947,10 @@ BalanceWs balance_ws(int L, int d, int N_r, int N_c, bool backward) {
         w.T_lo = take(2 * (size_t)N_c * pr);
         w.ds_hi = take(P);
         w.ds_lo = take(P);
-        w.xs = take(2 * (size_t)L * d);
+        w.x16 = take(2 * (size_t)L * d);
+        w.w16 = take(2 * (size_t)w.ld * d);
     } else {
-        const int bn = tile_width(N_r, 32);
+        const int bn = fwd_width(L, N_r);
         w.parts = 2 * ((N_r + bn - 1) / bn);
         w.part = take(4 * (size_t)w.parts * L);
         w.blocks = take(8 * (size_t)((L + kLossThreads - 1) / kLossThreads));
@@ -673,14 +963,18 @@ cudaError_t launch_counts(const int32_t *idx, const uint8_t *mask, int64_t M, in
                           int32_t *counts, int32_t *n_tokens, int *status, cudaStream_t st) {
     const int64_t want = (N + 1023) / 1024, most = (int64_t)device_sm_count() * 8;
     cudaError_t e = launch(counts_clear_kernel, dim3((unsigned)(want < most ? want : most)),
-                           dim3(256), 0, st, counts, N, n_tokens);
+                           dim3(256), 0, st, counts, N, n_tokens, status);
     if (e != cudaSuccess) return e;
-    return launch(counts_kernel, dim3((unsigned)((M + 255) / 256)), dim3(256), 0, st, idx, mask, M,
-                  K, N, counts, n_tokens, status);
+    return launch(counts_kernel, dim3((unsigned)((M + 255) / 256)), dim3(256), 0, st, idx, mask,
+                  (int)M, K, (int)N, counts, n_tokens, status);
 }
 
 namespace {
-// word 1 of the header: some count above kExactCount; 2: kept tokens; 3: CTAs done
+unsigned prep_grid(int64_t want) {
+    const int64_t most = (int64_t)device_sm_count() * kPrepPerSm;
+    return (unsigned)(want < most ? want : most);
+}
+
 cudaError_t launch_prep(BalPrep &p, void *ws, const BalanceWs &w, cudaStream_t st) {
     p.ld = w.ld;
     p.pr = pad64(p.N_r);
@@ -690,13 +984,11 @@ cudaError_t launch_prep(BalPrep &p, void *ws, const BalanceWs &w, cudaStream_t s
     p.P_lo = ws_at<uint16_t>(ws, w.P_lo);
     p.F_hi = ws_at<uint16_t>(ws, w.F_hi);
     p.F_lo = ws_at<uint16_t>(ws, w.F_lo);
-    p.big = ws_at<int>(ws, 4);
-    p.n_local = ws_at<int>(ws, 8);
-    const int64_t units = (int64_t)p.L * (p.ld / 8), tiles = (int64_t)(p.pr / 32) * (p.pc / 32);
-    int64_t want = (units + kPrepThreads - 1) / kPrepThreads;
-    if (want < tiles) want = tiles;
-    const int64_t most = (int64_t)device_sm_count() * 8;
-    return launch(balance_prep_kernel, dim3((unsigned)(want < most ? want : most)),
+    p.hdr = ws_at<BalHeader>(ws, 0);
+    const int64_t units =
+        ((int64_t)p.L * ((p.ld + 255) / 256) + kPrepThreads / 32 - 1) / (kPrepThreads / 32);
+    const int64_t tiles = (int64_t)(p.pr / 64) * (p.pc / 64);
+    return launch(balance_prep_kernel, dim3(prep_grid(units > tiles ? units : tiles)),
                   dim3(kPrepThreads), 0, st, p);
 }
 }  // namespace
@@ -713,22 +1005,21 @@ cudaError_t launch_balance_fwd(const float *p_r, const float *p_c, const int32_t
     if (e != cudaSuccess) return e;
     GemmArgs g = {};
     GemmProb &p = g.prob[0];
-    p.M = L; p.N = N_r; p.nk = pp.pc / BK; p.a_hi = 0; p.a_lo = 1; p.b = 2; p.b2 = 3; p.p = p_r;
-    set_tiles(&p, 32);
-    g.nprob = 1; g.tiles = p.tiles; g.big = pp.big; g.mask = mask;
+    p.M = L; p.N = N_r; p.nk = pp.pc / BK; p.a_hi = 0; p.a_lo = 1; p.b = 2; p.b_lo = 3; p.p = p_r;
+    set_tiles(&p, N_r, fwd_width(L, N_r));
+    g.nprob = 1; g.tiles = p.tiles; g.mask = mask; g.hdr = pp.hdr;
     g.part = ws_at<float>(ws, w.part);
-    g.status = ws_at<int>(ws, 0);
     GemmMaps maps;
     if (!make_sw128_map(&maps.m[0], pp.P_hi, L, w.ld, BM) ||
         !make_sw128_map(&maps.m[1], pp.P_lo, L, w.ld, BM) ||
-        !make_sw128_map(&maps.m[2], pp.F_hi, N_r, pp.pc, p.bn) ||
-        !make_sw128_map(&maps.m[3], pp.F_lo, N_r, pp.pc, p.bn))
+        !make_sw128_map(&maps.m[2], pp.F_hi, N_r, pp.pc, p.bn / 2) ||
+        !make_sw128_map(&maps.m[3], pp.F_lo, N_r, pp.pc, p.bn / 2))
         return cudaErrorInvalidValue;
     if ((e = launch_gemm<kFwd>(maps, g, st)) != cudaSuccess) return e;
     return launch(balance_loss_kernel, dim3((unsigned)((L + kLossThreads - 1) / kLossThreads)),
                   dim3(kLossThreads), 0, st, (const float *)g.part, w.parts, L, token_loss,
-                  ws_at<double>(ws, w.blocks), ws_at<int>(ws, 12),
-                  (double)N_r * (double)N_c / (double)K, n_tokens, (const int *)pp.n_local, loss);
+                  ws_at<double>(ws, w.blocks), pp.hdr, (double)N_r * (double)N_c / (double)K,
+                  n_tokens, loss);
 }
 
 cudaError_t launch_balance_bwd(const uint16_t *x, const uint16_t *W_r, const uint16_t *W_c,
@@ -736,78 +1027,82 @@ cudaError_t launch_balance_bwd(const uint16_t *x, const uint16_t *W_r, const uin
                                const int32_t *n_tokens, const uint8_t *mask,
                                const float *token_loss, int L, int d, int N_r, int N_c, int K,
                                float dloss, float *dx, bool accumulate, float *dW_r, float *dW_c,
-                               void *ws, cudaStream_t st) {
+                               bool overwrite, void *ws, cudaStream_t st) {
     const BalanceWs w = balance_ws(L, d, N_r, N_c, true);
     BalPrep pp = {};
     pp.p_r = p_r; pp.p_c = p_c; pp.counts = counts; pp.mask = mask;
-    pp.L = L; pp.N_r = N_r; pp.N_c = N_c; pp.d = d; pp.x = x;
+    pp.L = L; pp.N_r = N_r; pp.N_c = N_c; pp.d = d; pp.x = x; pp.W_r = W_r; pp.W_c = W_c;
     pp.T_hi = ws_at<uint16_t>(ws, w.T_hi);
     pp.T_lo = ws_at<uint16_t>(ws, w.T_lo);
-    // what masked rows of x hold must not meet a zero gradient as NaN
-    pp.xs = mask ? ws_at<uint16_t>(ws, w.xs) : nullptr;
     cudaError_t e = launch_prep(pp, ws, w, st);
     if (e != cudaSuccess) return e;
+    BalCast ca = {};
+    ca.x = x; ca.W_r = W_r; ca.W_c = W_c; ca.mask = mask;
+    ca.L = L; ca.N_r = N_r; ca.N_c = N_c; ca.d = d; ca.pr = pp.pr; ca.ld = w.ld;
+    ca.x16 = ws_at<uint16_t>(ws, w.x16);
+    ca.w16 = ws_at<uint16_t>(ws, w.w16);
+    ca.hdr = pp.hdr;
+    const int64_t rows = (int64_t)L + w.ld;
+    e = launch(balance_cast_kernel, dim3(prep_grid((rows + kPrepThreads / 32 - 1) / (kPrepThreads / 32))),
+               dim3(kPrepThreads), 0, st, ca);
+    if (e != cudaSuccess) return e;
     uint16_t *ds_hi = ws_at<uint16_t>(ws, w.ds_hi), *ds_lo = ws_at<uint16_t>(ws, w.ds_lo);
+    const int mtiles = (L + 2 * BM - 1) / (2 * BM);
 
     GemmArgs g = {};
-    g.mask = mask; g.big = pp.big; g.token_loss = token_loss;
-    g.n_tokens = n_tokens; g.n_local = pp.n_local;
-    g.factor = (float)((double)dloss * N_r * N_c / K);
-    g.status = ws_at<int>(ws, 0);
+    g.mask = mask; g.token_loss = token_loss; g.hdr = pp.hdr; g.ld = w.ld;
     g.nprob = 2;
+    // the pad columns belong to the tiles too: they must be written as zeros
+    const int segs[2] = {pp.pr, pp.pc};
+    const int bn = pick_width(segs, 2, mtiles, device_sm_count() / 2);
     for (int a = 0; a < 2; ++a) {                    // U with ds_r, V with ds_c
         GemmProb &p = g.prob[a];
         p.M = L; p.N = a == 0 ? N_r : N_c;
-        p.nk = (a == 0 ? pp.pc : pp.pr) / BK;
+        p.nk = segs[1 - a] / BK;
         p.a_hi = 0; p.a_lo = 1; p.a_c0 = a == 0 ? pp.pr : 0;
-        p.b = 2 + 2 * a; p.b2 = 3 + 2 * a;
-        p.p = a == 0 ? p_r : p_c;
-        p.seg = a == 0 ? pp.pr : pp.pc;
+        p.b = 2 + 2 * a; p.b_lo = 3 + 2 * a;
+        p.P_hi = pp.P_hi + (a == 0 ? 0 : pp.pr);
+        p.P_lo = pp.P_lo + (a == 0 ? 0 : pp.pr);
+        p.seg = segs[a];
         p.ds_hi = ds_hi + (a == 0 ? 0 : pp.pr);
         p.ds_lo = ds_lo + (a == 0 ? 0 : pp.pr);
-        p.ld_out = w.ld;
-        // the pad columns belong to the tiles too: they must be written as zeros
-        p.N = p.seg;
-        set_tiles(&p, 32);
-        p.N = a == 0 ? N_r : N_c;
+        set_tiles(&p, p.seg, bn);
         g.tiles += p.tiles;
     }
     GemmMaps maps;
     if (!make_sw128_map(&maps.m[0], pp.P_hi, L, w.ld, BM) ||
         !make_sw128_map(&maps.m[1], pp.P_lo, L, w.ld, BM) ||
-        !make_sw128_map(&maps.m[2], pp.F_hi, N_r, pp.pc, g.prob[0].bn) ||
-        !make_sw128_map(&maps.m[3], pp.F_lo, N_r, pp.pc, g.prob[0].bn) ||
-        !make_sw128_map(&maps.m[4], pp.T_hi, N_c, pp.pr, g.prob[1].bn) ||
-        !make_sw128_map(&maps.m[5], pp.T_lo, N_c, pp.pr, g.prob[1].bn))
+        !make_sw128_map(&maps.m[2], pp.F_hi, N_r, pp.pc, bn / 2) ||
+        !make_sw128_map(&maps.m[3], pp.F_lo, N_r, pp.pc, bn / 2) ||
+        !make_sw128_map(&maps.m[4], pp.T_hi, N_c, pp.pr, bn / 2) ||
+        !make_sw128_map(&maps.m[5], pp.T_lo, N_c, pp.pr, bn / 2))
         return cudaErrorInvalidValue;
     if ((e = launch_gemm<kGrid>(maps, g, st)) != cudaSuccess) return e;
 
     GemmArgs h = {};
-    h.status = g.status;
-    h.nprob = 3;
-    for (int a = 0; a < 2; ++a) {                    // dW_r, dW_c: A is ds^T, K the tokens
-        GemmProb &p = h.prob[a];
-        p.M = a == 0 ? N_r : N_c; p.N = d;
-        p.nk = p.nk1 = (L + BK - 1) / BK;
-        p.a_hi = 2; p.a_lo = 3; p.a_c0 = a == 0 ? 0 : pp.pr;
-        p.b = p.b2 = 4;
-        p.out = a == 0 ? dW_r : dW_c; p.ld_out = d; p.accumulate = 1;
-    }
-    GemmProb &p = h.prob[2];                         // dx: B is W_r, then W_c
-    p.M = L; p.N = d; p.nk = w.ld / BK; p.nk1 = pp.pr / BK;
-    p.a_hi = 0; p.a_lo = 1; p.b = 5; p.b2 = 6;
-    p.out = dx; p.ld_out = d; p.accumulate = accumulate ? 1 : 0;
-    for (int a = 0; a < 3; ++a) {
-        set_tiles(&h.prob[a], 64);
-        h.tiles += h.prob[a].tiles;
-    }
+    h.hdr = pp.hdr; h.n_tokens = n_tokens;
+    h.factor = (float)((double)dloss * N_r * N_c / K);
+    h.nprob = 2;
+    GemmProb &dw = h.prob[0];                        // A is ds^T, K the tokens
+    dw.M = w.ld; dw.N = d; dw.nk = (L + BK - 1) / BK;
+    dw.a_hi = 2; dw.a_lo = 3; dw.b = 4;
+    dw.out = dW_r; dw.out2 = dW_c; dw.split = pp.pr; dw.rows1 = N_r; dw.rows2 = N_c;
+    dw.accumulate = overwrite ? 0 : 1;
+    GemmProb &px = h.prob[1];
+    px.M = L; px.N = d; px.nk = w.ld / BK;
+    px.a_hi = 0; px.a_lo = 1; px.b = 5;
+    px.out = dx; px.split = L; px.rows1 = L;
+    px.accumulate = accumulate ? 1 : 0;
+    const int bg = d > 128 ? 256 : 128;              // MN-major: whole 64-element boxes in each CTA
+    set_tiles(&dw, d, bg);
+    set_tiles(&px, d, bg);
+    h.tiles = dw.tiles + px.tiles;
     if (!make_sw128_map(&maps.m[0], ds_hi, L, w.ld, BM) ||
         !make_sw128_map(&maps.m[1], ds_lo, L, w.ld, BM) ||
         !make_sw128_map(&maps.m[2], ds_hi, L, w.ld, 64) ||
         !make_sw128_map(&maps.m[3], ds_lo, L, w.ld, 64) ||
-        !make_sw128_map(&maps.m[4], pp.xs ? pp.xs : x, L, d, 64) ||
-        !make_sw128_map(&maps.m[5], W_r, N_r, d, 64) ||
-        !make_sw128_map(&maps.m[6], W_c, N_c, d, 64))
+        !make_sw128_map(&maps.m[4], ca.x16, L, d, 64) ||
+        !make_sw128_map(&maps.m[5], ca.w16, w.ld, d, 64))
         return cudaErrorInvalidValue;
     return launch_gemm<kGrads>(maps, h, st);
 }

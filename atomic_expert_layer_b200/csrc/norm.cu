@@ -14,12 +14,16 @@
 // the value, or 2^-10 of the scale near zero).  Infinities and NaN are kept as
 // NaN and do not take part in the block's scale.
 //
-// A row stays in registers between its one read and its one write: TPR
-// threads share it, each holding VPT vectors of 8 values, so the variance is
-// taken about the mean (no cancellation) and x is read once.  Everything is
-// bound by HBM (or by launch latency below a few hundred rows).
+// A row stays in registers between its one read and its one write: a group of
+// G threads shares it, each holding VPT vectors of 8 values (one, up to d =
+// 4096), so the variance is taken about the mean (no cancellation) and x is
+// read once.  A CTA's groups take rows side by side, and each loads its next
+// row before it reduces the present one.  Everything is bound by HBM (or by
+// launch latency below a few hundred rows).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
+
+#include <type_traits>
 
 #include "omni_common.cuh"
 #include "omni_internal.h"
@@ -27,7 +31,7 @@
 namespace omni {
 namespace {
 
-constexpr int kNormThreads = 128;
+constexpr int kNormThreads = 512;
 
 // ------------------------------------------------------------- 8 values
 __device__ __forceinline__ void load8(const uint16_t *p, float *v) {
@@ -105,62 +109,128 @@ __device__ __forceinline__ void ckpt_unpack8(uint2 q, int code, float *v) {
 }
 
 // ------------------------------------------------- sums over a row's threads
-// TPR = 32: the row belongs to one warp; TPR = kNormThreads: to the CTA.
-template <int TPR, int NV>
-__device__ __forceinline__ void row_sum(float (&v)[NV], float *red) {
+// Sums over a group; red: two sets of slots, used in turn, so that one barrier
+// a sum is enough (a group cannot be two sums ahead of one of its warps).
+template <int G, int NV>
+struct GroupSum {
+    static constexpr int W = G / 32;
+    float *red;
+    int turn;
+    __device__ GroupSum(float *smem, int group) : red(smem + group * 2 * NV * W), turn(0) {}
+    __device__ void operator()(float (&v)[NV], int group) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) v[i] = warp_sum(v[i]);
-    if (TPR > 32) {
-        constexpr int W = TPR / 32;
-        const int warp = (int)(threadIdx.x >> 5);
-        __syncthreads();                                  // red is free again
-        if (lane_id() == 0)
-            for (int i = 0; i < NV; ++i) red[i * W + warp] = v[i];
-        __syncthreads();
+        for (int i = 0; i < NV; ++i) v[i] = warp_sum(v[i]);
+        if (G > 32) {
+            float *r = red + turn * NV * W;
+            turn ^= 1;
+            const int warp = (int)(threadIdx.x % G) >> 5;
+            if (lane_id() == 0) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            v[i] = 0.f;
+                for (int i = 0; i < NV; ++i) r[i * W + warp] = v[i];
+            }
+            // barriers 1 to 15; a CTA of 16 groups has warps for groups
+            if (G == kNormThreads) __syncthreads();
+            else asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(G) : "memory");
 #pragma unroll
-            for (int k = 0; k < W; ++k) v[i] += red[i * W + k];
+            for (int i = 0; i < NV; ++i) {
+                v[i] = 0.f;
+#pragma unroll
+                for (int k = 0; k < W; ++k) v[i] += r[i * W + k];
+            }
         }
     }
-}
+};
+
+// A thread's vectors of a row as they lie in memory.
+template <typename T, int VPT>
+struct RawRow;
+template <int VPT>
+struct RawRow<float, VPT> {
+    float4 a[VPT], b[VPT];
+    __device__ void load(const float *row, int c, int step, int nvec) {
+#pragma unroll
+        for (int k = 0; k < VPT; ++k)
+            if (c + k * step < nvec) {
+                const float4 *p = reinterpret_cast<const float4 *>(row) + 2 * (c + k * step);
+                a[k] = p[0];
+                b[k] = p[1];
+            }
+    }
+    __device__ void get(int k, float *v) const {
+        v[0] = a[k].x; v[1] = a[k].y; v[2] = a[k].z; v[3] = a[k].w;
+        v[4] = b[k].x; v[5] = b[k].y; v[6] = b[k].z; v[7] = b[k].w;
+    }
+};
+template <int VPT>
+struct RawRow<uint16_t, VPT> {
+    uint4 u[VPT];
+    __device__ void load(const uint16_t *row, int c, int step, int nvec) {
+#pragma unroll
+        for (int k = 0; k < VPT; ++k)
+            if (c + k * step < nvec) u[k] = reinterpret_cast<const uint4 *>(row)[c + k * step];
+    }
+    __device__ void get(int k, float *v) const {
+        const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+};
+// ... of a checkpoint: T is uint8_t, 8 bytes and their block's scale
+template <int VPT>
+struct RawRow<uint8_t, VPT> {
+    uint2 q[VPT];
+    uint8_t s[VPT];
+    __device__ void load(const uint8_t *row, int c, int step, int nvec, const uint8_t *scale) {
+#pragma unroll
+        for (int k = 0; k < VPT; ++k)
+            if (c + k * step < nvec) {
+                q[k] = reinterpret_cast<const uint2 *>(row)[c + k * step];
+                s[k] = scale[(c + k * step) >> 2];
+            }
+    }
+    __device__ void get(int k, float *v) const { ckpt_unpack8(q[k], s[k], v); }
+};
 
 // ---------------------------------------------------------------- forward
-template <typename T, int TPR, int VPT>
-__global__ void __launch_bounds__(kNormThreads)
+template <typename T, int G, int VPT, bool CKPT>
+__global__ void __launch_bounds__(kNormThreads, VPT == 1 ? 2 : 1)
 norm_fwd_kernel(const T *__restrict__ x, const uint16_t *__restrict__ w,
                 const uint16_t *__restrict__ b, int L, int d, float eps, uint16_t *__restrict__ y,
                 float *__restrict__ mean_out, float *__restrict__ rstd_out,
                 uint8_t *__restrict__ q, uint8_t *__restrict__ scale) {
-    __shared__ float red[8];
+    __shared__ float red[2 * kNormThreads / 32];
     grid_dependency_wait();
     grid_dependents_launch();
-    constexpr int RPC = kNormThreads / TPR;               // rows of a CTA
-    const int tr = (int)threadIdx.x % TPR;
+    constexpr int GROUPS = kNormThreads / G;
+    const int group = (int)threadIdx.x / G, c = (int)threadIdx.x % G;
     const int nvec = d >> 3;
     const float inv_d = 1.f / (float)d;
-    // the rows of a CTA take the same number of turns, so its barriers match
-    for (int64_t r0 = (int64_t)blockIdx.x * RPC; r0 < L; r0 += (int64_t)gridDim.x * RPC) {
-        const int64_t row = r0 + (int)threadIdx.x / TPR;
-        const bool live = row < L;
+    GroupSum<G, 1> sum(red, group);
+    RawRow<T, VPT> raw;
+    const int64_t step = (int64_t)gridDim.x * GROUPS;
+    int64_t row = (int64_t)blockIdx.x * GROUPS + group;
+    if (row < L) raw.load(x + row * d, c, G, nvec);
+    for (; row < L; row += step) {                       // the same for a whole group
         float v[VPT][8];
         float s[1] = {0.f};
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
-            const int c = tr + k * TPR;
-            if (live && c < nvec) {
-                load8(x + row * d + 8 * c, v[k]);
+            if (c + k * G < nvec) {
+                raw.get(k, v[k]);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) s[0] += v[k][i];
             }
         }
-        row_sum<TPR, 1>(s, red);
+        if (row + step < L) raw.load(x + (row + step) * d, c, G, nvec);
+        sum(s, group);
         const float mean = s[0] * inv_d;
         s[0] = 0.f;
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
-            if (live && tr + k * TPR < nvec) {
+            if (c + k * G < nvec) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     v[k][i] -= mean;
@@ -168,85 +238,91 @@ norm_fwd_kernel(const T *__restrict__ x, const uint16_t *__restrict__ w,
                 }
             }
         }
-        row_sum<TPR, 1>(s, red);
+        sum(s, group);
         const float rstd = rsqrtf(fmaf(s[0], inv_d, eps));
-        if (live && tr == 0) {
+        if (c == 0) {
             if (mean_out) mean_out[row] = mean;
             if (rstd_out) rstd_out[row] = rstd;
         }
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
-            const int c = tr + k * TPR;
-            const bool on = live && c < nvec;
+            const int cc = c + k * G;
+            const bool on = cc < nvec;
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[k][i] = on ? v[k][i] * rstd : 0.f;
-            if (q) {
+            if (CKPT) {
                 int code;
                 const uint2 p = ckpt_pack8(v[k], &code);
                 if (on) {
-                    *reinterpret_cast<uint2 *>(q + row * d + 8 * c) = p;
-                    if ((c & 3) == 0) scale[row * (d >> 5) + (c >> 2)] = (uint8_t)code;
+                    *reinterpret_cast<uint2 *>(q + row * d + 8 * cc) = p;
+                    if ((cc & 3) == 0) scale[row * (d >> 5) + (cc >> 2)] = (uint8_t)code;
                 }
             }
-            if (on && y) {
+            if (on) {
                 float wf[8], bf[8];
-                load8(w + 8 * c, wf);
-                if (b) load8(b + 8 * c, bf);
+                load8(w + 8 * cc, wf);
+                if (b) load8(b + 8 * cc, bf);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) v[k][i] = b ? fmaf(v[k][i], wf[i], bf[i]) : v[k][i] * wf[i];
-                store8(y + row * d + 8 * c, v[k]);
+                store8(y + row * d + 8 * cc, v[k]);
             }
         }
     }
 }
 
 // --------------------------------------------------------------- backward
-// KEPT: 0 = x in T with mean, 1 = checkpoint.  Each CTA adds up dy xh and dy
-// over its rows in registers and writes them to part[blockIdx.x * RPC + r][2][d]
-// (r: the row slot in the CTA).
-template <typename T, bool CKPT, int TPR, int VPT>
-__global__ void __launch_bounds__(kNormThreads)
-norm_bwd_kernel(const T *__restrict__ x, const float *__restrict__ mean_in,
-                const float *__restrict__ rstd_in, const uint8_t *__restrict__ q,
-                const uint8_t *__restrict__ scale, const uint16_t *__restrict__ w,
-                const float *__restrict__ dy, int L, int d, float *__restrict__ dx,
+// T: the kept rows' type, fp32 or bf16 with mean, or uint8_t for a checkpoint.
+// A CTA adds up dy xh and dy over its rows in registers, then over its groups
+// in shared memory, and writes them to part[blockIdx.x][2][d].
+template <typename T, int G, int VPT>
+__global__ void __launch_bounds__(kNormThreads, VPT == 1 ? 2 : 1)
+norm_bwd_kernel(const T *__restrict__ x, const uint8_t *__restrict__ scale,
+                const float *__restrict__ mean_in, const float *__restrict__ rstd_in,
+                const uint16_t *__restrict__ w, const float *dy, int L, int d, float *dx,
                 int accumulate, float *__restrict__ part) {
-    __shared__ float red[2 * kNormThreads / 32];
+    constexpr bool CKPT = sizeof(T) == 1;
+    constexpr int GROUPS = kNormThreads / G;
+    __shared__ float red[4 * kNormThreads / 32];
+    // half of the groups' sums at most: GROUPS / 2 rows of 2 d <= 16 G floats
+    __shared__ float4 half_sums[GROUPS > 1 ? kNormThreads * 2 : 1];
     grid_dependency_wait();
     grid_dependents_launch();
-    constexpr int RPC = kNormThreads / TPR;
-    const int tr = (int)threadIdx.x % TPR;
+    const int group = (int)threadIdx.x / G, c = (int)threadIdx.x % G;
     const int nvec = d >> 3;
     const float inv_d = 1.f / (float)d;
+    GroupSum<G, 2> sum(red, group);
     float aw[VPT][8], ab[VPT][8];
 #pragma unroll
     for (int k = 0; k < VPT; ++k)
 #pragma unroll
         for (int i = 0; i < 8; ++i) aw[k][i] = ab[k][i] = 0.f;
-    for (int64_t r0 = (int64_t)blockIdx.x * RPC; r0 < L; r0 += (int64_t)gridDim.x * RPC) {
-        const int64_t row = r0 + (int)threadIdx.x / TPR;
-        const bool live = row < L;
-        const float rstd = live ? rstd_in[row] : 0.f;
-        const float mean = live && !CKPT ? mean_in[row] : 0.f;
+    RawRow<T, VPT> raw;
+    RawRow<float, VPT> raw_dy;
+    float mean = 0.f, rstd = 0.f;
+    const auto load = [&](int64_t r) {
+        if constexpr (CKPT) raw.load(x + r * d, c, G, nvec, scale + r * (d >> 5));
+        else raw.load(x + r * d, c, G, nvec);
+        raw_dy.load(dy + r * d, c, G, nvec);
+        rstd = rstd_in[r];
+        if (!CKPT) mean = mean_in[r];
+    };
+    const int64_t step = (int64_t)gridDim.x * GROUPS;
+    int64_t row = (int64_t)blockIdx.x * GROUPS + group;
+    if (row < L) load(row);
+    for (; row < L; row += step) {                       // the same for a whole group
         float h[VPT][8], g[VPT][8];
         float s[2] = {0.f, 0.f};
+        const float rs = rstd;
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
-            const int c = tr + k * TPR;
-            if (live && c < nvec) {
-                if (CKPT) {
-                    ckpt_unpack8(*reinterpret_cast<const uint2 *>(q + row * d + 8 * c),
-                                 scale[row * (d >> 5) + (c >> 2)], h[k]);
-                } else {
-                    load8(x + row * d + 8 * c, h[k]);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) h[k][i] = (h[k][i] - mean) * rstd;
-                }
-                load8(dy + row * d + 8 * c, g[k]);
+            if (c + k * G < nvec) {
+                raw.get(k, h[k]);
+                raw_dy.get(k, g[k]);
                 float wf[8];
-                load8(w + 8 * c, wf);
+                load8(w + 8 * (c + k * G), wf);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
+                    if (!CKPT) h[k][i] = (h[k][i] - mean) * rs;
                     aw[k][i] = fmaf(g[k][i], h[k][i], aw[k][i]);
                     ab[k][i] += g[k][i];
                     g[k][i] *= wf[i];
@@ -255,57 +331,84 @@ norm_bwd_kernel(const T *__restrict__ x, const float *__restrict__ mean_in,
                 }
             }
         }
-        row_sum<TPR, 2>(s, red);
+        if (row + step < L) load(row + step);
+        sum(s, group);
         const float m0 = s[0] * inv_d, m1 = s[1] * inv_d;
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
-            const int c = tr + k * TPR;
-            if (live && c < nvec) {
-                float *out = dx + row * d + 8 * c;
+            if (c + k * G < nvec) {
+                float *out = dx + row * d + 8 * (c + k * G);
                 float o[8];
                 if (accumulate) load8(out, o);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     // rounded on its own, so that an addition to dx is one addition
-                    const float t = __fmul_rn(rstd, g[k][i] - m0 - h[k][i] * m1);
+                    const float t = __fmul_rn(rs, g[k][i] - m0 - h[k][i] * m1);
                     o[i] = accumulate ? o[i] + t : t;
                 }
                 store8(out, o);
             }
         }
     }
-    float *pw = part + ((int64_t)blockIdx.x * RPC + (int)threadIdx.x / TPR) * 2 * d;
+    // groups h .. 2h - 1 hand their sums to groups 0 .. h - 1 (VPT is 1 where
+    // there are several groups)
+#pragma unroll
+    for (int n = GROUPS / 2; n >= 1; n /= 2) {
+        float *slot = reinterpret_cast<float *>(half_sums) + ((group % n) * G + c) * 16;
+        __syncthreads();
+        if (group >= n && group < 2 * n) {
+            store8(slot, aw[0]);
+            store8(slot + 8, ab[0]);
+        }
+        __syncthreads();
+        if (group < n) {
+            float t[16];
+            load8(slot, t);
+            load8(slot + 8, t + 8);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                aw[0][i] += t[i];
+                ab[0][i] += t[8 + i];
+            }
+        }
+    }
+    if (group != 0) return;
+    float *pw = part + (int64_t)blockIdx.x * 2 * d;
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-        const int c = tr + k * TPR;
-        if (c < nvec) {
-            store8(pw + 8 * c, aw[k]);
-            store8(pw + d + 8 * c, ab[k]);
+        const int cc = c + k * G;
+        if (cc < nvec) {
+            store8(pw + 8 * cc, aw[k]);
+            store8(pw + d + 8 * cc, ab[k]);
         }
     }
 }
 
-// dw += sum of part[i][0], db += sum of part[i][1], in the order of i: one
-// column per thread of 32, eight slices of i per column.
-__global__ void __launch_bounds__(256)
+// dw, db += (or =) the sums of part[i][0], part[i][1] in a fixed order: 32
+// columns of a CTA, their rows in 32 slices.
+constexpr int kSumSlices = 32;
+__global__ void __launch_bounds__(32 * kSumSlices)
 norm_bwd_sum_kernel(const float *__restrict__ part, int nparts, int d, float *__restrict__ dw,
-                    float *__restrict__ db) {
-    __shared__ float sm[8][32];
+                    float *__restrict__ db, int overwrite) {
+    __shared__ float sm[kSumSlices][33];
     grid_dependency_wait();
     grid_dependents_launch();
-    const int c = blockIdx.x * 32 + (int)(threadIdx.x & 31);
-    const int slice = (int)(threadIdx.x >> 5);
+    const int lane = (int)(threadIdx.x & 31), slice = (int)(threadIdx.x >> 5);
+    const int c = blockIdx.x * 32 + lane;
     const int cols = db ? 2 * d : d;
     float s = 0.f;
-    if (c < cols)
-        for (int i = slice; i < nparts; i += 8) s += part[(int64_t)i * 2 * d + c];
-    sm[slice][threadIdx.x & 31] = s;
+    if (c < cols) {
+#pragma unroll 4
+        for (int i = slice; i < nparts; i += kSumSlices) s += part[(int64_t)i * 2 * d + c];
+    }
+    sm[slice][lane] = s;
     __syncthreads();
-    if (slice == 0 && c < cols) {
-#pragma unroll
-        for (int k = 1; k < 8; ++k) s += sm[k][threadIdx.x & 31];
-        float *o = c < d ? dw + c : db + (c - d);
-        *o += s;
+    // warp w adds up column w
+    s = warp_sum(sm[lane][slice]);
+    const int col = blockIdx.x * 32 + slice;
+    if (lane == 0 && col < cols) {
+        float *o = col < d ? dw + col : db + (col - d);
+        *o = overwrite ? s : *o + s;
     }
 }
 
@@ -359,61 +462,60 @@ unsigned blocks_for(int64_t units, int per_block, int per_sm) {
     return (unsigned)(want < most ? want : most);
 }
 
+// Threads that share a row: one vector of 8 each, a power of two of them (two
+// vectors for d > 4096).  Fewer, with more vectors each, leave too little in
+// flight: 128 threads at d = 2048 took 77 us for the backward where 256 take
+// less than 60 (L = 16384, from a checkpoint).
+int group_threads(int d) {
+    int g = 32;
+    while (g < kNormThreads && 8 * g < d) g *= 2;
+    return g;
+}
+
+unsigned norm_blocks(int L, int d) {
+    return blocks_for(L, kNormThreads / group_threads(d), d <= 4096 ? 2 : 1);
+}
+
 }  // namespace
 
-// rows of partial sums that the backward writes for these sizes
-int norm_bwd_parts(int L, int d) {
-    const int rpc = d <= 1024 ? kNormThreads / 32 : 1;
-    return (int)blocks_for(L, rpc, 4) * rpc;
-}
+int norm_bwd_parts(int L, int d) { return (int)norm_blocks(L, d); }
 
 namespace {
 
-template <typename T>
+template <typename T, bool CKPT>
 cudaError_t norm_fwd_t(const T *x, const uint16_t *w, const uint16_t *b, int L, int d, float eps,
                        uint16_t *y, float *mean, float *rstd, uint8_t *q, uint8_t *scale,
                        cudaStream_t st) {
-    const int rpc = d <= 1024 ? kNormThreads / 32 : 1;
-    const dim3 grid(blocks_for(L, rpc, 8)), block(kNormThreads);
-    const int vecs = d <= 1024 ? (d + 255) / 256 : (d + 1023) / 1024;
-#define OMNI_NORM(tpr, n) \
-    case n: return launch(norm_fwd_kernel<T, tpr, n>, grid, block, 0, st, x, w, b, L, d, eps, y, \
-                          mean, rstd, q, scale);
-    if (d <= 1024) {
-        switch (vecs) { OMNI_NORM(32, 1) OMNI_NORM(32, 2) OMNI_NORM(32, 3) OMNI_NORM(32, 4) }
-    } else {
-        switch (vecs) {
-            OMNI_NORM(kNormThreads, 2) OMNI_NORM(kNormThreads, 3) OMNI_NORM(kNormThreads, 4)
-            OMNI_NORM(kNormThreads, 5) OMNI_NORM(kNormThreads, 6) OMNI_NORM(kNormThreads, 7)
-            OMNI_NORM(kNormThreads, 8)
-        }
+    const auto go = [&](auto kernel) {
+        return launch(kernel, dim3(norm_blocks(L, d)), dim3(kNormThreads), 0, st, x, w, b, L, d, eps,
+                      y, mean, rstd, q, scale);
+    };
+    if (d > 4096) return go(norm_fwd_kernel<T, 512, 2, CKPT>);
+    switch (group_threads(d)) {
+        case 32: return go(norm_fwd_kernel<T, 32, 1, CKPT>);
+        case 64: return go(norm_fwd_kernel<T, 64, 1, CKPT>);
+        case 128: return go(norm_fwd_kernel<T, 128, 1, CKPT>);
+        case 256: return go(norm_fwd_kernel<T, 256, 1, CKPT>);
+        default: return go(norm_fwd_kernel<T, 512, 1, CKPT>);
     }
-#undef OMNI_NORM
-    return cudaErrorInvalidValue;
 }
 
-template <typename T, bool CKPT>
-cudaError_t norm_bwd_t(const T *x, const float *mean, const float *rstd, const uint8_t *q,
-                       const uint8_t *scale, const uint16_t *w, const float *dy, int L, int d,
-                       float *dx, bool accumulate, float *part, cudaStream_t st) {
-    const int rpc = d <= 1024 ? kNormThreads / 32 : 1;
-    const dim3 grid((unsigned)(norm_bwd_parts(L, d) / rpc)), block(kNormThreads);
-    const int vecs = d <= 1024 ? (d + 255) / 256 : (d + 1023) / 1024;
-    const int acc = accumulate ? 1 : 0;
-#define OMNI_NORM(tpr, n) \
-    case n: return launch(norm_bwd_kernel<T, CKPT, tpr, n>, grid, block, 0, st, x, mean, rstd, q, \
-                          scale, w, dy, L, d, dx, acc, part);
-    if (d <= 1024) {
-        switch (vecs) { OMNI_NORM(32, 1) OMNI_NORM(32, 2) OMNI_NORM(32, 3) OMNI_NORM(32, 4) }
-    } else {
-        switch (vecs) {
-            OMNI_NORM(kNormThreads, 2) OMNI_NORM(kNormThreads, 3) OMNI_NORM(kNormThreads, 4)
-            OMNI_NORM(kNormThreads, 5) OMNI_NORM(kNormThreads, 6) OMNI_NORM(kNormThreads, 7)
-            OMNI_NORM(kNormThreads, 8)
-        }
+template <typename T>
+cudaError_t norm_bwd_t(const T *x, const uint8_t *scale, const float *mean, const float *rstd,
+                       const uint16_t *w, const float *dy, int L, int d, float *dx, bool accumulate,
+                       float *part, cudaStream_t st) {
+    const auto go = [&](auto kernel) {
+        return launch(kernel, dim3(norm_blocks(L, d)), dim3(kNormThreads), 0, st, x, scale, mean,
+                      rstd, w, dy, L, d, dx, accumulate ? 1 : 0, part);
+    };
+    if (d > 4096) return go(norm_bwd_kernel<T, 512, 2>);
+    switch (group_threads(d)) {
+        case 32: return go(norm_bwd_kernel<T, 32, 1>);
+        case 64: return go(norm_bwd_kernel<T, 64, 1>);
+        case 128: return go(norm_bwd_kernel<T, 128, 1>);
+        case 256: return go(norm_bwd_kernel<T, 256, 1>);
+        default: return go(norm_bwd_kernel<T, 512, 1>);
     }
-#undef OMNI_NORM
-    return cudaErrorInvalidValue;
 }
 
 }  // namespace
@@ -421,29 +523,31 @@ cudaError_t norm_bwd_t(const T *x, const float *mean, const float *rstd, const u
 cudaError_t launch_norm_fwd(const void *x, bool x_f32, const uint16_t *w, const uint16_t *b, int L,
                             int d, float eps, uint16_t *y, float *mean, float *rstd, uint8_t *q,
                             uint8_t *scale, cudaStream_t st) {
-    if (x_f32)
-        return norm_fwd_t(static_cast<const float *>(x), w, b, L, d, eps, y, mean, rstd, q, scale, st);
-    return norm_fwd_t(static_cast<const uint16_t *>(x), w, b, L, d, eps, y, mean, rstd, q, scale, st);
+    const auto go = [&](auto *xt) {
+        using T = std::remove_const_t<std::remove_pointer_t<decltype(xt)>>;
+        return q ? norm_fwd_t<T, true>(xt, w, b, L, d, eps, y, mean, rstd, q, scale, st)
+                 : norm_fwd_t<T, false>(xt, w, b, L, d, eps, y, mean, rstd, q, scale, st);
+    };
+    return x_f32 ? go(static_cast<const float *>(x)) : go(static_cast<const uint16_t *>(x));
 }
 
 cudaError_t launch_norm_bwd(const void *x, bool x_f32, const float *mean, const float *rstd,
                             const uint8_t *q, const uint8_t *scale, const uint16_t *w,
                             const float *dy, int L, int d, float *dx, bool accumulate, float *dw,
-                            float *db, float *part, cudaStream_t st) {
+                            float *db, bool overwrite, float *part, cudaStream_t st) {
     cudaError_t e;
     if (q)
-        e = norm_bwd_t<uint16_t, true>(nullptr, mean, rstd, q, scale, w, dy, L, d, dx, accumulate,
-                                       part, st);
+        e = norm_bwd_t(q, scale, mean, rstd, w, dy, L, d, dx, accumulate, part, st);
     else if (x_f32)
-        e = norm_bwd_t<float, false>(static_cast<const float *>(x), mean, rstd, q, scale, w, dy, L,
-                                     d, dx, accumulate, part, st);
+        e = norm_bwd_t(static_cast<const float *>(x), scale, mean, rstd, w, dy, L, d, dx,
+                       accumulate, part, st);
     else
-        e = norm_bwd_t<uint16_t, false>(static_cast<const uint16_t *>(x), mean, rstd, q, scale, w,
-                                        dy, L, d, dx, accumulate, part, st);
+        e = norm_bwd_t(static_cast<const uint16_t *>(x), scale, mean, rstd, w, dy, L, d, dx,
+                       accumulate, part, st);
     if (e != cudaSuccess) return e;
     const int cols = db ? 2 * d : d;
-    return launch(norm_bwd_sum_kernel, dim3((unsigned)((cols + 31) / 32)), dim3(256), 0, st,
-                  (const float *)part, norm_bwd_parts(L, d), d, dw, db);
+    return launch(norm_bwd_sum_kernel, dim3((unsigned)((cols + 31) / 32)), dim3(32 * kSumSlices), 0,
+                  st, (const float *)part, norm_bwd_parts(L, d), d, dw, db, overwrite ? 1 : 0);
 }
 
 cudaError_t launch_ckpt_pack(const void *x, bool x_f32, int L, int d, uint8_t *q, uint8_t *scale,

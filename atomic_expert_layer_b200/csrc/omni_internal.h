@@ -202,18 +202,19 @@ int norm_bwd_parts(int L, int d);
 cudaError_t launch_norm_bwd(const void *x, bool x_f32, const float *mean, const float *rstd,
                             const uint8_t *q, const uint8_t *scale, const uint16_t *w,
                             const float *dy, int L, int d, float *dx, bool accumulate, float *dw,
-                            float *db, float *part, cudaStream_t st);
+                            float *db, bool overwrite, float *part, cudaStream_t st);
 cudaError_t launch_ckpt_pack(const void *x, bool x_f32, int L, int d, uint8_t *q, uint8_t *scale,
                              cudaStream_t st);
 // w (and then b) may be null
 cudaError_t launch_ckpt_unpack(const uint8_t *q, const uint8_t *scale, const uint16_t *w,
                                const uint16_t *b, int L, int d, uint16_t *x, cudaStream_t st);
 
-// ---- balance loss (balance.cu); the workspaces' headers are zeroed
+// ---- balance loss (balance.cu); launch_counts clears the status word itself, the
+// others expect their workspace's header zeroed
 struct BalanceWs {
     int ld;                  // columns of P and ds: both padded axes (forward: the column axis)
     int parts;               // sums per token that the forward's tiles leave
-    size_t P_hi, P_lo, F_hi, F_lo, T_hi, T_lo, ds_hi, ds_lo, xs, part, blocks, total;
+    size_t P_hi, P_lo, F_hi, F_lo, T_hi, T_lo, ds_hi, ds_lo, x16, w16, part, blocks, total;
 };
 BalanceWs balance_ws(int L, int d, int N_r, int N_c, bool backward);
 cudaError_t launch_counts(const int32_t *idx, const uint8_t *mask, int64_t M, int K, int64_t N,
@@ -227,7 +228,7 @@ cudaError_t launch_balance_bwd(const uint16_t *x, const uint16_t *W_r, const uin
                                const int32_t *n_tokens, const uint8_t *mask,
                                const float *token_loss, int L, int d, int N_r, int N_c, int K,
                                float dloss, float *dx, bool accumulate, float *dW_r, float *dW_c,
-                               void *ws, cudaStream_t st);
+                               bool overwrite, void *ws, cudaStream_t st);
 
 int device_sm_count();
 

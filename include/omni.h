@@ -74,6 +74,7 @@ typedef enum {
 #define OMNI_EXPERT_SPARSE     32u  /* expert stage: every task on the task-by-task path (no tiles)       */
 #define OMNI_X_F32             64u  /* layer norm, checkpoints: x is fp32 (a residual stream), not bf16   */
 #define OMNI_DX_ACCUMULATE    128u  /* layer norm and balance backward: dx += gradient instead of dx =    */
+#define OMNI_DW_OVERWRITE     256u  /* ... : weight gradients = instead of +=                             */
 
 /* Device status codes written into the workspace status word. */
 #define OMNI_DEV_OK              0
@@ -361,13 +362,15 @@ int omni_expert_counts(const int32_t *idx, const uint8_t *mask, int L, int K, in
  *   ds_c[t, j] likewise with V = P_r F
  *   dx [L, d] fp32    = ds_r W_r + ds_c W_c, or added to dx with OMNI_DX_ACCUMULATE
  *                       (so that it joins omni_routed_bwd's); masked rows get 0
- *   dW_r [N_r, d], dW_c [N_c, d] fp32  += ds^T x, accumulated
+ *   dW_r [N_r, d], dW_c [N_c, d] fp32  += ds^T x, accumulated (= with
+ *                       OMNI_DW_OVERWRITE, what they held is not read)
  *   x [L, d], W_r, W_c bf16 (the forward's; the rows of masked tokens of x do
  *   not matter); token_loss is the forward's.
- * Products run on the tensor cores with fp32 sums: exp(p) enters as two fp16
- * values (hi + lo, 22 bits; exp(p) must stay below 4), ds as two bf16 values
- * (16 bits).  Every output element is written by one tile: the results are the
- * same on every run.
+ * Products run on the tensor cores with fp32 sums: exp(p) and ds enter as two
+ * fp16 values each (hi + lo, 22 bits; exp(p) must stay below 4), x and W as
+ * fp16 scaled by a power of two (exact for values down to 2^-32 of the largest
+ * finite one).  Every output element is written by one tile: the results are
+ * the same on every run.
  * ws: the size functions' bytes, 256-byte aligned.  dx, dW_r, dW_c, x, W_r,
  * W_c 16-byte aligned.  d % 8 == 0.  Limits: N_r, N_c <= OMNI_MAX_AXIS,
  * N < 2^31.
@@ -407,7 +410,8 @@ int omni_layer_norm_fwd(const void *x, const omni_bf16 *w, const omni_bf16 *b, i
  *   dy [L, d] fp32 (omni_routed_bwd's dx);  rstd [L] fp32 of the forward
  *   dx [L, d] fp32 output, or added to dx with OMNI_DX_ACCUMULATE; dx may be dy
  *   (without the flag)
- *   dw [d], db [d] fp32  accumulated (+=): sum_t dy xh, sum_t dy; db may be NULL
+ *   dw [d], db [d] fp32  accumulated (+=; = with OMNI_DW_OVERWRITE): sum_t dy xh,
+ *   sum_t dy; db may be NULL
  * The sums over the rows run in a fixed order: the results are the same on
  * every run.  ws: omni_layer_norm_bwd_workspace_size(L, d) bytes, 256-byte
  * aligned.  Limits as for the forward; fp32 arrays 16-byte aligned (mean,
