@@ -31,7 +31,14 @@
 namespace omni {
 namespace {
 
-constexpr int kNormThreads = 512;
+// Threads of a CTA whose rows take groups of G, and CTAs of an SM for the
+// forward and the backward (VPT vectors a thread): what their registers allow
+// without spilling, which mattered more than the number of warps (backward at
+// L = 16384, d = 2048 from a checkpoint: 84 us at 64 registers with 120 bytes
+// spilled, 55 us at 79 with none).
+__host__ __device__ constexpr int cta_threads(int G) { return G > 256 ? G : 256; }
+__host__ __device__ constexpr int fwd_ctas(int G, int VPT) { return VPT > 1 ? 1 : G > 256 ? 2 : 4; }
+__host__ __device__ constexpr int bwd_ctas(int G, int VPT) { return VPT > 1 || G > 256 ? 1 : 3; }
 
 // ------------------------------------------------------------- 8 values
 __device__ __forceinline__ void load8(const uint16_t *p, float *v) {
@@ -77,21 +84,35 @@ __device__ __forceinline__ float ckpt_scale(int code) {     // 2^(code - 127)
 __device__ __forceinline__ float finite_or_nan(float v) {
     return fabsf(v) <= 3.402823466e38f ? v : __uint_as_float(0x7fc00000u);
 }
+__device__ __forceinline__ float block_max(float m) {        // of four neighbouring lanes
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    return fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+}
 // Packs this thread's 8 values; four neighbouring lanes hold one block.
-// Every lane of the warp takes part in the shuffles.
-__device__ __forceinline__ uint2 ckpt_pack8(const float *v, int *code) {
+// Every lane of the warp takes part in the shuffles.  NaN needs no care: fmaxf
+// drops it and the conversion keeps it.  Infinities are looked for once a
+// block (testing every value made the kernel issue-bound: 75 us at L = 65536,
+// d = 2048, where 407 MB take 63).
+__device__ __forceinline__ uint2 ckpt_pack8(float *v, int *code) {
     float amax = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(finite_or_nan(v[i])));   // fmaxf drops NaN
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
+    amax = block_max(amax);
+    if (__any_sync(0xffffffffu, amax > 3.402823466e38f)) {
+        amax = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            v[i] = finite_or_nan(v[i]);
+            amax = fmaxf(amax, fabsf(v[i]));
+        }
+        amax = block_max(amax);
+    }
     *code = ckpt_code(amax);
     const float inv = __uint_as_float((uint32_t)(254 - *code) << 23);              // 2^(127 - code)
     uint32_t h[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        h[i] = __nv_cvt_float2_to_fp8x2(make_float2(finite_or_nan(v[2 * i]) * inv,
-                                                    finite_or_nan(v[2 * i + 1]) * inv),
+        h[i] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i] * inv, v[2 * i + 1] * inv),
                                         __NV_SATFINITE, __NV_E4M3);
     return make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
 }
@@ -128,8 +149,8 @@ struct GroupSum {
 #pragma unroll
                 for (int i = 0; i < NV; ++i) r[i * W + warp] = v[i];
             }
-            // barriers 1 to 15; a CTA of 16 groups has warps for groups
-            if (G == kNormThreads) __syncthreads();
+            // barriers 1 to 4: a CTA of 8 groups has warps for groups
+            if (G == cta_threads(G)) __syncthreads();
             else asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(G) : "memory");
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
@@ -196,15 +217,15 @@ struct RawRow<uint8_t, VPT> {
 
 // ---------------------------------------------------------------- forward
 template <typename T, int G, int VPT, bool CKPT>
-__global__ void __launch_bounds__(kNormThreads, VPT == 1 ? 2 : 1)
+__global__ void __launch_bounds__(cta_threads(G), fwd_ctas(G, VPT))
 norm_fwd_kernel(const T *__restrict__ x, const uint16_t *__restrict__ w,
                 const uint16_t *__restrict__ b, int L, int d, float eps, uint16_t *__restrict__ y,
                 float *__restrict__ mean_out, float *__restrict__ rstd_out,
                 uint8_t *__restrict__ q, uint8_t *__restrict__ scale) {
-    __shared__ float red[2 * kNormThreads / 32];
+    constexpr int GROUPS = cta_threads(G) / G;
+    __shared__ float red[2 * cta_threads(G) / 32];
     grid_dependency_wait();
     grid_dependents_launch();
-    constexpr int GROUPS = kNormThreads / G;
     const int group = (int)threadIdx.x / G, c = (int)threadIdx.x % G;
     const int nvec = d >> 3;
     const float inv_d = 1.f / (float)d;
@@ -275,16 +296,16 @@ norm_fwd_kernel(const T *__restrict__ x, const uint16_t *__restrict__ w,
 // A CTA adds up dy xh and dy over its rows in registers, then over its groups
 // in shared memory, and writes them to part[blockIdx.x][2][d].
 template <typename T, int G, int VPT>
-__global__ void __launch_bounds__(kNormThreads, VPT == 1 ? 2 : 1)
+__global__ void __launch_bounds__(cta_threads(G), bwd_ctas(G, VPT))
 norm_bwd_kernel(const T *__restrict__ x, const uint8_t *__restrict__ scale,
                 const float *__restrict__ mean_in, const float *__restrict__ rstd_in,
                 const uint16_t *__restrict__ w, const float *dy, int L, int d, float *dx,
                 int accumulate, float *__restrict__ part) {
     constexpr bool CKPT = sizeof(T) == 1;
-    constexpr int GROUPS = kNormThreads / G;
-    __shared__ float red[4 * kNormThreads / 32];
+    constexpr int GROUPS = cta_threads(G) / G;
+    __shared__ float red[4 * cta_threads(G) / 32];
     // half of the groups' sums at most: GROUPS / 2 rows of 2 d <= 16 G floats
-    __shared__ float4 half_sums[GROUPS > 1 ? kNormThreads * 2 : 1];
+    __shared__ float4 half_sums[GROUPS > 1 ? cta_threads(G) * 2 : 1];
     grid_dependency_wait();
     grid_dependents_launch();
     const int group = (int)threadIdx.x / G, c = (int)threadIdx.x % G;
@@ -413,15 +434,18 @@ norm_bwd_sum_kernel(const float *__restrict__ part, int nparts, int d, float *__
 }
 
 // ------------------------------------------------- packing and restoring
+// All CTAs of both grids are resident: 32 registers.
+constexpr int kCkptThreads = 256, kCkptPerSm = 8;
+
 template <typename T>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kCkptThreads, kCkptPerSm)
 ckpt_pack_kernel(const T *__restrict__ x, int64_t nvec, uint8_t *__restrict__ q,
                  uint8_t *__restrict__ scale) {
     grid_dependency_wait();
     grid_dependents_launch();
     // whole warps take each turn (the shuffles need every lane)
-    for (int64_t c0 = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) & ~(int64_t)31; c0 < nvec;
-         c0 += (int64_t)gridDim.x * blockDim.x) {
+    for (int64_t c0 = ((int64_t)blockIdx.x * kCkptThreads + threadIdx.x) & ~(int64_t)31; c0 < nvec;
+         c0 += (int64_t)gridDim.x * kCkptThreads) {
         const int64_t c = c0 + lane_id();
         float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         if (c < nvec) load8(x + 8 * c, v);
@@ -434,14 +458,14 @@ ckpt_pack_kernel(const T *__restrict__ x, int64_t nvec, uint8_t *__restrict__ q,
     }
 }
 
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kCkptThreads, kCkptPerSm)
 ckpt_unpack_kernel(const uint8_t *__restrict__ q, const uint8_t *__restrict__ scale,
                    const uint16_t *__restrict__ w, const uint16_t *__restrict__ b, int64_t nvec,
                    int dvec, uint16_t *__restrict__ x) {
     grid_dependency_wait();
     grid_dependents_launch();
-    for (int64_t c = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; c < nvec;
-         c += (int64_t)gridDim.x * blockDim.x) {
+    for (int64_t c = (int64_t)blockIdx.x * kCkptThreads + threadIdx.x; c < nvec;
+         c += (int64_t)gridDim.x * kCkptThreads) {
         float v[8];
         ckpt_unpack8(*reinterpret_cast<const uint2 *>(q + 8 * c), scale[c >> 2], v);
         if (w) {
@@ -463,22 +487,20 @@ unsigned blocks_for(int64_t units, int per_block, int per_sm) {
 }
 
 // Threads that share a row: one vector of 8 each, a power of two of them (two
-// vectors for d > 4096).  Fewer, with more vectors each, leave too little in
-// flight: 128 threads at d = 2048 took 77 us for the backward where 256 take
-// less than 60 (L = 16384, from a checkpoint).
+// vectors for d > 4096).
 int group_threads(int d) {
     int g = 32;
-    while (g < kNormThreads && 8 * g < d) g *= 2;
+    while (g < 512 && 8 * g < d) g *= 2;
     return g;
 }
-
-unsigned norm_blocks(int L, int d) {
-    return blocks_for(L, kNormThreads / group_threads(d), d <= 4096 ? 2 : 1);
+unsigned norm_blocks(int L, int d, bool backward) {
+    const int g = group_threads(d), vpt = d > 4096 ? 2 : 1;
+    return blocks_for(L, cta_threads(g) / g, backward ? bwd_ctas(g, vpt) : fwd_ctas(g, vpt));
 }
 
 }  // namespace
 
-int norm_bwd_parts(int L, int d) { return (int)norm_blocks(L, d); }
+int norm_bwd_parts(int L, int d) { return (int)norm_blocks(L, d, true); }
 
 namespace {
 
@@ -486,12 +508,13 @@ template <typename T, bool CKPT>
 cudaError_t norm_fwd_t(const T *x, const uint16_t *w, const uint16_t *b, int L, int d, float eps,
                        uint16_t *y, float *mean, float *rstd, uint8_t *q, uint8_t *scale,
                        cudaStream_t st) {
+    const int g = group_threads(d);
     const auto go = [&](auto kernel) {
-        return launch(kernel, dim3(norm_blocks(L, d)), dim3(kNormThreads), 0, st, x, w, b, L, d, eps,
-                      y, mean, rstd, q, scale);
+        return launch(kernel, dim3(norm_blocks(L, d, false)), dim3(cta_threads(g)), 0, st, x, w, b, L,
+                      d, eps, y, mean, rstd, q, scale);
     };
     if (d > 4096) return go(norm_fwd_kernel<T, 512, 2, CKPT>);
-    switch (group_threads(d)) {
+    switch (g) {
         case 32: return go(norm_fwd_kernel<T, 32, 1, CKPT>);
         case 64: return go(norm_fwd_kernel<T, 64, 1, CKPT>);
         case 128: return go(norm_fwd_kernel<T, 128, 1, CKPT>);
@@ -504,12 +527,13 @@ template <typename T>
 cudaError_t norm_bwd_t(const T *x, const uint8_t *scale, const float *mean, const float *rstd,
                        const uint16_t *w, const float *dy, int L, int d, float *dx, bool accumulate,
                        float *part, cudaStream_t st) {
+    const int g = group_threads(d);
     const auto go = [&](auto kernel) {
-        return launch(kernel, dim3(norm_blocks(L, d)), dim3(kNormThreads), 0, st, x, scale, mean,
-                      rstd, w, dy, L, d, dx, accumulate ? 1 : 0, part);
+        return launch(kernel, dim3(norm_blocks(L, d, true)), dim3(cta_threads(g)), 0, st, x, scale,
+                      mean, rstd, w, dy, L, d, dx, accumulate ? 1 : 0, part);
     };
     if (d > 4096) return go(norm_bwd_kernel<T, 512, 2>);
-    switch (group_threads(d)) {
+    switch (g) {
         case 32: return go(norm_bwd_kernel<T, 32, 1>);
         case 64: return go(norm_bwd_kernel<T, 64, 1>);
         case 128: return go(norm_bwd_kernel<T, 128, 1>);
@@ -553,7 +577,7 @@ cudaError_t launch_norm_bwd(const void *x, bool x_f32, const float *mean, const 
 cudaError_t launch_ckpt_pack(const void *x, bool x_f32, int L, int d, uint8_t *q, uint8_t *scale,
                              cudaStream_t st) {
     const int64_t nvec = (int64_t)L * (d >> 3);
-    const dim3 grid(blocks_for(nvec, 256, 8)), block(256);
+    const dim3 grid(blocks_for(nvec, kCkptThreads, kCkptPerSm)), block(kCkptThreads);
     if (x_f32)
         return launch(ckpt_pack_kernel<float>, grid, block, 0, st, static_cast<const float *>(x),
                       nvec, q, scale);
@@ -564,7 +588,8 @@ cudaError_t launch_ckpt_pack(const void *x, bool x_f32, int L, int d, uint8_t *q
 cudaError_t launch_ckpt_unpack(const uint8_t *q, const uint8_t *scale, const uint16_t *w,
                                const uint16_t *b, int L, int d, uint16_t *x, cudaStream_t st) {
     const int64_t nvec = (int64_t)L * (d >> 3);
-    return launch(ckpt_unpack_kernel, dim3(blocks_for(nvec, 256, 8)), dim3(256), 0, st, q, scale, w,
+    return launch(ckpt_unpack_kernel, dim3(blocks_for(nvec, kCkptThreads, kCkptPerSm)),
+                  dim3(kCkptThreads), 0, st, q, scale, w,
                   b, nvec, d >> 3, x);
 }
 
