@@ -290,7 +290,7 @@ def _grads(names, given, like):
     """The weight gradients to write: the given fp32 buffers, which are
     accumulated into, or new ones.  All new: OMNI_DW_OVERWRITE spares zeroing
     and reading them; some given: the new ones start at zero."""
-    if given[0] is None and given[-1] is None:
+    if not any(g is not None for g in given):
         return [torch.empty_like(t, dtype=_F32) for t in like], OMNI_DW_OVERWRITE
     return [_grad(*ngl) for ngl in zip(names, given, like)], 0
 
@@ -476,11 +476,11 @@ def routed_bwd_ckpt(q, scale, W, V, W_r, W_c, idx, gate, dy, w=None, b=None, dW=
           _at("idx", idx, _I32, (L, K), di), _at("gate", gate, _F32, (L, K), di),
           _at("dy", dy, _F32, (L, d), di))
     dx = torch.empty_like(dy)
-    dW, dV = _grad("dW", dW, W), _grad("dV", dV, V)
-    dW_r, dW_c = _grad("dW_r", dW_r, W_r), _grad("dW_c", dW_c, W_c)
+    (dW, dV, dW_r, dW_c), flags = _grads(("dW", "dV", "dW_r", "dW_c"), (dW, dV, dW_r, dW_c),
+                                         (W, V, W_r, W_c))
     lib = load()
     ws, ws_at, ws_n = _scratch(ws, lib.omni_routed_bwd_ckpt_workspace_size(L, d, N_r, N_c, K), di)
     _check("omni_routed_bwd_ckpt", lib.omni_routed_bwd_ckpt(
-        *at, dx.data_ptr(), dW.data_ptr(), dV.data_ptr(), dW_r.data_ptr(), dW_c.data_ptr(), 0, ws_at,
-        ws_n, _queue(di)))
+        *at, dx.data_ptr(), dW.data_ptr(), dV.data_ptr(), dW_r.data_ptr(), dW_c.data_ptr(), flags,
+        ws_at, ws_n, _queue(di)))
     return dict(dx=dx, dW=dW, dV=dV, dW_r=dW_r, dW_c=dW_c)

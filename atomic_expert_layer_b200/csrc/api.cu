@@ -738,7 +738,7 @@ int omni_routed_bwd_ckpt(const uint8_t *q, const uint8_t *scale, const omni_bf16
     if (rc) return rc;
     // everything omni_routed_bwd checks, before the restoring launch
     if (!W || !V || !W_r || !W_c || !idx || !gate || !dy || !dx || !dW || !dV || !dW_r || !dW_c ||
-        !ws || flags != 0)
+        !ws || (flags & ~OMNI_DW_OVERWRITE) != 0)
         return OMNI_ERR_INVALID_ARG;
     if (d % 256 != 0 || d > OMNI_MAX_D) return OMNI_ERR_UNSUPPORTED;
     if (!aligned16(W) || !aligned16(V) || !aligned16(W_r) || !aligned16(W_c) || !aligned16(dy) ||
@@ -749,8 +749,17 @@ int omni_routed_bwd_ckpt(const uint8_t *q, const uint8_t *scale, const omni_bf16
     const size_t bwd = omni_routed_bwd_workspace_size(L, d, N_r, N_c, K);
     uint16_t *x = ws_at<uint16_t>(ws, bwd);
     if ((rc = omni_act_unpack(q, scale, w, b, L, d, x, stream))) return rc;
+    if (flags & OMNI_DW_OVERWRITE) {
+        cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+        const size_t row = sizeof(float) * (size_t)d;
+        if (cudaMemsetAsync(dW, 0, row * (size_t)sz.N, st) != cudaSuccess ||
+            cudaMemsetAsync(dV, 0, row * (size_t)sz.N, st) != cudaSuccess ||
+            cudaMemsetAsync(dW_r, 0, row * (size_t)N_r, st) != cudaSuccess ||
+            cudaMemsetAsync(dW_c, 0, row * (size_t)N_c, st) != cudaSuccess)
+            return OMNI_ERR_CUDA;
+    }
     return omni_routed_bwd(x, W, V, W_r, W_c, L, d, N_r, N_c, K, idx, gate, dy, dx, dW, dV, dW_r,
-                           dW_c, flags, ws, bwd, stream);
+                           dW_c, 0u, ws, bwd, stream);
 }
 
 int omni_selftest_wait_timeout(void *ws, size_t ws_bytes, int limit_ms, omni_stream_t stream) {

@@ -30,11 +30,22 @@
 //   x and W, bf16: so that their largest finite magnitude becomes 2^14 to
 //     2^15.  fp16 then holds every bf16 value down to 2^-32 of it exactly.
 // bf16 halves (16 bits) need no scales, but left dx and dW off by 2.9e-6 of
-// themselves, and by 4e-3 for a collapsed router, where U - l_t cancels; fp32
-// arithmetic leaves 1e-6 and 2e-4 there.
+// themselves, and by 4e-3 for a collapsed router, where U - l_t cancels.  With
+// these, and with what kChunk below says, the results are as near to 64 bits
+// as fp32 arithmetic's (headline: 5e-7, torch in fp32 1.2e-6).
+//
+// Bounds and measurements, headline layer (L = 4096, d = 1024, 1304 x 1304
+// grid, one B200, clocks under load): the products are 28 GFLOP forward, 56 +
+// 87 GFLOP backward, twice the definition's because of the halves, against
+// 1407 TFLOP/s sustained.  Forward 40 us (20 at that rate), U and V with ds 78
+// us (40), dW and dx 87 us (62); what is above goes to the rounds that do not
+// fill 74 pairs (192 tiles of 256 x 224; 44 tiles of 64 and 64 of 42 K steps),
+// to draining the accumulators every second K step (each drain holds up the
+// products; every fourth step: 21 us less for the three, errors 3 times as
+// large), and in the second to 88 MB of P and ds that the epilogue reads and
+// writes.  Preparing the operands takes 42 us for the two calls (173 MB).
 //
 // Masked rows of p are never read as numbers: their P and ds are zero.
-#include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include "omni_common.cuh"
@@ -99,9 +110,23 @@ __global__ void counts_clear_kernel(int32_t *__restrict__ counts, int64_t N,
 
 constexpr int kCountSpan = 4096;        // mask bytes that a CTA counts at a time
 
+// Kept tokens, counted from the mask, 4096 by a CTA: an atomic per token, all
+// on one address, took 60 us of 67 at 16384 tokens.
+__device__ __forceinline__ void count_tokens(const uint8_t *mask, int L, int32_t *n_tokens) {
+    if (!mask) {
+        if (blockIdx.x == 0 && threadIdx.x == 0) *n_tokens = L;
+        return;
+    }
+    int kept = 0;
+    for (int64_t t = (int64_t)blockIdx.x * kCountSpan; t < L; t += (int64_t)gridDim.x * kCountSpan)
+        for (int i = (int)threadIdx.x; i < kCountSpan && t + i < L; i += (int)blockDim.x)
+            kept += mask[t + i] != 0;
+    kept = warp_isum(kept);
+    if (kept && lane_id() == 0) atomicAdd(n_tokens, kept);
+}
+
 // One thread per task; integer atomics, so the counts do not depend on the
-// order.  Kept tokens are counted from the mask, 4096 by a CTA: an atomic per
-// token, all on one address, took 60 us of 67 at 16384 tokens.
+// order.
 __global__ void __launch_bounds__(256)
 counts_kernel(const int32_t *__restrict__ idx, const uint8_t *__restrict__ mask, int M, int K, int N,
               int32_t *__restrict__ counts, int32_t *__restrict__ n_tokens, int *status) {
@@ -113,17 +138,44 @@ counts_kernel(const int32_t *__restrict__ idx, const uint8_t *__restrict__ mask,
         if (e >= 0 && e < N) atomicAdd(&counts[e], 1);
         else set_status(status, OMNI_DEV_BAD_EXPERT);
     }
-    const int L = M / K;
-    if (!mask) {
-        if (at == 0) *n_tokens = L;
-        return;
+    count_tokens(mask, M / K, n_tokens);
+}
+
+// The same for crowded experts, whose atomics would wait for one another (2 to
+// 4 ns each on one address): a CTA first counts its tasks in a table in shared
+// memory, one expert to a slot; a task whose slot another expert holds goes to
+// memory by itself.
+constexpr int kCrowdThreads = 512, kCrowdTasks = 8192, kCrowdSlots = 4096;
+__global__ void __launch_bounds__(kCrowdThreads)
+counts_crowded_kernel(const int32_t *__restrict__ idx, const uint8_t *__restrict__ mask, int M, int K,
+                      int N, int32_t *__restrict__ counts, int32_t *__restrict__ n_tokens, int *status) {
+    __shared__ int key[kCrowdSlots], hits[kCrowdSlots];
+    for (int i = (int)threadIdx.x; i < kCrowdSlots; i += kCrowdThreads) {
+        key[i] = -1;
+        hits[i] = 0;
     }
-    const int64_t t0 = (int64_t)blockIdx.x * kCountSpan;
-    if (t0 >= L) return;
-    int kept = 0;
-    for (int i = (int)threadIdx.x; i < kCountSpan && t0 + i < L; i += 256) kept += mask[t0 + i] != 0;
-    kept = warp_isum(kept);
-    if (kept && lane_id() == 0) atomicAdd(n_tokens, kept);
+    grid_dependency_wait();
+    grid_dependents_launch();
+    __syncthreads();
+    const unsigned first = blockIdx.x * (unsigned)kCrowdTasks;
+#pragma unroll 4
+    for (unsigned i = threadIdx.x; i < (unsigned)kCrowdTasks; i += kCrowdThreads) {
+        const unsigned at = first + i;                        // M < 2^31: no wrap
+        if (at >= (unsigned)M || (mask && !mask[at / (unsigned)K])) continue;
+        const int e = idx[at];
+        if (e < 0 || e >= N) {
+            set_status(status, OMNI_DEV_BAD_EXPERT);
+            continue;
+        }
+        const unsigned slot = (unsigned)e * 2654435761u >> 20;
+        const int held = atomicCAS(&key[slot], -1, e);
+        if (held == -1 || held == e) atomicAdd(&hits[slot], 1);
+        else atomicAdd(&counts[e], 1);
+    }
+    __syncthreads();
+    for (int i = (int)threadIdx.x; i < kCrowdSlots; i += kCrowdThreads)
+        if (hits[i]) atomicAdd(&counts[key[i]], hits[i]);
+    count_tokens(mask, M / K, n_tokens);
 }
 
 // -------------------------------------------------------------- operands
@@ -393,11 +445,11 @@ constexpr uint32_t kIdescF16 =                   // A and B fp16 (formats 0); th
 constexpr int kMaxProbs = 2, kMaxMaps = 6;
 // K steps that are summed in TMEM before the epilogue warps add them to their
 // registers.  The tensor core cuts off what falls below its accumulator at
-// every instruction (8 of them in a step), always towards zero: over the 512
-// instructions of a dW tile at L = 4096 that took 1.1e-5 off the result, and
-// it grows with L; over 32 it is below 1e-6, and the additions in registers
-// round to nearest.  Draining is hidden behind the next steps' products.
-constexpr int kChunk = 4;
+// every instruction, always towards zero: over the 512 instructions of a dW
+// tile at L = 4096 that took 1.1e-5 off the result, and it grows with L.  Here
+// an accumulator takes 16 instructions, the 8 of the lo halves first, while it
+// is still small; the additions in registers round to nearest.
+constexpr int kChunk = 2;
 
 struct __align__(1024) GemmSmem {
     uint8_t a[STAGES][2 * kBytesA];
@@ -599,40 +651,46 @@ balance_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant
                 // a 16-deep slice: 32 bytes along a K-major atom, or 16 K rows
                 const uint64_t a_step = (a_mn ? 16 * 128 : 32) >> 4;
                 const uint64_t b_step = (MODE == kGrads ? 16 * 128 : 32) >> 4;
-                uint32_t acc = 0;
-                for (int st = 0; st < steps; ++st, ++it) {
-                    const int s = it % STAGES;
-                    const bool first = st % kChunk == 0;
-                    if (first) {                              // the next accumulator
-                        if (lt >= 2 && !mbar_wait(&sm.tempty[lt & 1],
-                                                          (uint32_t)(((lt >> 1) - 1) & 1), status)) {
-                            ok = false;
-                            break;
-                        }
-                        acc = tmem + (uint32_t)((lt & 1) * BN);
-                    }
-                    if (!mbar_wait(&sm.full[s], (uint32_t)((it / STAGES) & 1), status)) {
+                for (int st = 0; st < steps; st += kChunk, ++lt) {
+                    if (lt >= 2 &&
+                        !mbar_wait(&sm.tempty[lt & 1], (uint32_t)(((lt >> 1) - 1) & 1), status)) {
                         ok = false;
                         break;
                     }
-                    tc_fence_after();
-                    const uint64_t ah = a_mn ? sw128_desc_mn(sm.a[s]) : sw128_desc(sm.a[s]);
-                    const uint64_t bd = MODE == kGrads ? sw128_desc_mn(sm.b[s]) : sw128_desc(sm.b[s]);
+                    const uint32_t acc = tmem + (uint32_t)((lt & 1) * BN);
+                    const int n = min(kChunk, steps - st);
+                    uint32_t started = 0;
+                    for (int i = 0; i < n; ++i) {             // lo halves
+                        const int s = (it + i) % STAGES;
+                        if (!mbar_wait(&sm.full[s], (uint32_t)(((it + i) / STAGES) & 1), status)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        if (MODE != kGrads && st + i >= p.nk) continue;   // hi times F_lo only
+                        const uint8_t *a = sm.a[s] + kBytesA;
+                        const uint64_t ad = a_mn ? sw128_desc_mn(a) : sw128_desc(a);
+                        const uint64_t bd = MODE == kGrads ? sw128_desc_mn(sm.b[s]) : sw128_desc(sm.b[s]);
 #pragma unroll
-                    for (int k = 0; k < BK / 16; ++k)
-                        umma_bf16_pair(acc, ah + k * a_step, bd + k * b_step, idesc,
-                                       (!first || k > 0) ? 1u : 0u);
-                    if (MODE == kGrads || st < p.nk) {
-                        const uint64_t al = ah + (kBytesA >> 4);
+                        for (int k = 0; k < BK / 16; ++k) {
+                            umma_bf16_pair(acc, ad + k * a_step, bd + k * b_step, idesc, started);
+                            started = 1;
+                        }
+                    }
+                    if (!ok) break;
+                    for (int i = 0; i < n; ++i) {             // hi halves
+                        const int s = (it + i) % STAGES;
+                        const uint64_t ad = a_mn ? sw128_desc_mn(sm.a[s]) : sw128_desc(sm.a[s]);
+                        const uint64_t bd = MODE == kGrads ? sw128_desc_mn(sm.b[s]) : sw128_desc(sm.b[s]);
 #pragma unroll
-                        for (int k = 0; k < BK / 16; ++k)
-                            umma_bf16_pair(acc, al + k * a_step, bd + k * b_step, idesc, 1u);
+                        for (int k = 0; k < BK / 16; ++k) {
+                            umma_bf16_pair(acc, ad + k * a_step, bd + k * b_step, idesc, started);
+                            started = 1;
+                        }
+                        umma_commit_pair(&sm.empty[s]);       // frees stage s in both CTAs
                     }
-                    umma_commit_pair(&sm.empty[s]);           // frees stage s in both CTAs
-                    if (st % kChunk == kChunk - 1 || st == steps - 1) {
-                        umma_commit_pair(&sm.tfull[lt & 1]);  // both CTAs' epilogues may read
-                        ++lt;
-                    }
+                    umma_commit_pair(&sm.tfull[lt & 1]);      // both CTAs' epilogues may read
+                    it += n;
                 }
             }
             if (!ok) sm.abort = 1;
@@ -646,12 +704,14 @@ balance_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant
         const uint32_t tempty0 = smem_in_cta(&sm.tempty[0], 0);
         const uint32_t tempty1 = smem_in_cta(&sm.tempty[1], 0);
         float *turn_buf = sm.turn[warp - 2];
-        float scale1 = 1.f, scale2 = 1.f;            // dW, dx: the scales that come out again
-        if (MODE == kGrid) scale1 = pow2f(1 - count_exp(g.hdr->most));   // 2^15, and P's 2^-14
+        // kGrid: ds / c to below 2^15, and P's 2^14 out; kGrads: that scale out,
+        // the operand's (scale2), and c in
+        float scale1 = 1.f, scale2 = 1.f, coef = 0.f;
+        if (MODE == kGrid) scale1 = pow2f(1 - count_exp(g.hdr->most));
         if (MODE == kGrads) {
             const int n = *g.n_tokens, kept = g.hdr->kept;
-            scale1 = n > 0 && kept > 0 ? g.factor / (float)n / (float)kept *
-                                             pow2f(count_exp(g.hdr->most) - 15) : 0.f;
+            if (n > 0 && kept > 0) coef = g.factor / (float)n / (float)kept;
+            scale1 = pow2f(count_exp(g.hdr->most) - 15);
         }
         int lt = 0;
         bool ok = true;
@@ -728,13 +788,26 @@ balance_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant
                     // each lane its own row: the sums stay where they are (no lane
                     // waits for another in here)
                     if (keep) {
-                        const float *src = p.p + (int64_t)row * p.N;
+                        const float *src = p.p + (int64_t)row * p.N + col0;
+                        if (vec && col0 + 32 <= p.N) {
 #pragma unroll
-                        for (int j = 0; j < 32; j += 8) {
-                            float v[8];
-                            load_logp8(src, col0 + j, p.N, vec, v);
+                            for (int j = 0; j < 32; j += 16) {
+                                float4 v[4];
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) part = fmaf(expf(v[k]), sum[q][j + k], part);
+                                for (int k = 0; k < 4; ++k)
+                                    v[k] = __ldg(reinterpret_cast<const float4 *>(src + j) + k);
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    part = fmaf(expf(v[k].x), sum[q][j + 4 * k], part);
+                                    part = fmaf(expf(v[k].y), sum[q][j + 4 * k + 1], part);
+                                    part = fmaf(expf(v[k].z), sum[q][j + 4 * k + 2], part);
+                                    part = fmaf(expf(v[k].w), sum[q][j + 4 * k + 3], part);
+                                }
+                            }
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (col0 + j < p.N) part = fmaf(expf(__ldg(src + j)), sum[q][j], part);
                         }
                     }
                 } else {
@@ -753,8 +826,8 @@ balance_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant
                         for (int i = 0; i < 4; ++i) {
                             const int64_t o = at + 4 * (i4 + i) * g.ld;
                             const bool in = row0 + r0 + 4 * (i4 + i) < p.M;
-                            hi[i] = in ? *reinterpret_cast<const uint2 *>(p.P_hi + o) : make_uint2(0, 0);
-                            lo[i] = in ? *reinterpret_cast<const uint2 *>(p.P_lo + o) : make_uint2(0, 0);
+                            hi[i] = in ? __ldg(reinterpret_cast<const uint2 *>(p.P_hi + o)) : make_uint2(0, 0);
+                            lo[i] = in ? __ldg(reinterpret_cast<const uint2 *>(p.P_lo + o)) : make_uint2(0, 0);
                         }
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
@@ -804,10 +877,10 @@ balance_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant
                         for (int i = 0; i < 4; ++i) {
                             const int r = r0 + 4 * (i4 + i);
                             float4 v;
-                            v.x = __fmul_rn(turn_buf[turned(r, c)] * scale1, scale2);
-                            v.y = __fmul_rn(turn_buf[turned(r, c + 1)] * scale1, scale2);
-                            v.z = __fmul_rn(turn_buf[turned(r, c + 2)] * scale1, scale2);
-                            v.w = __fmul_rn(turn_buf[turned(r, c + 3)] * scale1, scale2);
+                            v.x = __fmul_rn(turn_buf[turned(r, c)] * scale1 * scale2, coef);
+                            v.y = __fmul_rn(turn_buf[turned(r, c + 1)] * scale1 * scale2, coef);
+                            v.z = __fmul_rn(turn_buf[turned(r, c + 2)] * scale1 * scale2, coef);
+                            v.w = __fmul_rn(turn_buf[turned(r, c + 3)] * scale1 * scale2, coef);
                             if (p.accumulate) {
                                 v.x += prev[i].x;
                                 v.y += prev[i].y;
@@ -965,6 +1038,12 @@ cudaError_t launch_counts(const int32_t *idx, const uint8_t *mask, int64_t M, in
     cudaError_t e = launch(counts_clear_kernel, dim3((unsigned)(want < most ? want : most)),
                            dim3(256), 0, st, counts, N, n_tokens, status);
     if (e != cudaSuccess) return e;
+    // crowded: as many tasks as experts or more, and enough of them for a CTA
+    // on every SM (skewed layer, M = 2 N = 2^21: 17 against 61 us; with M = N =
+    // 2^18, 10 against 3)
+    if (M >= N && M >= (int64_t)1 << 20)
+        return launch(counts_crowded_kernel, dim3((unsigned)((M + kCrowdTasks - 1) / kCrowdTasks)),
+                      dim3(kCrowdThreads), 0, st, idx, mask, (int)M, K, (int)N, counts, n_tokens, status);
     return launch(counts_kernel, dim3((unsigned)((M + 255) / 256)), dim3(256), 0, st, idx, mask,
                   (int)M, K, (int)N, counts, n_tokens, status);
 }

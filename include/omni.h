@@ -74,7 +74,7 @@ typedef enum {
 #define OMNI_EXPERT_SPARSE     32u  /* expert stage: every task on the task-by-task path (no tiles)       */
 #define OMNI_X_F32             64u  /* layer norm, checkpoints: x is fp32 (a residual stream), not bf16   */
 #define OMNI_DX_ACCUMULATE    128u  /* layer norm and balance backward: dx += gradient instead of dx =    */
-#define OMNI_DW_OVERWRITE     256u  /* ... : weight gradients = instead of +=                             */
+#define OMNI_DW_OVERWRITE     256u  /* ..., routed backward from a checkpoint: weight gradients = not +=  */
 
 /* Device status codes written into the workspace status word. */
 #define OMNI_DEV_OK              0
@@ -369,7 +369,7 @@ int omni_expert_counts(const int32_t *idx, const uint8_t *mask, int L, int K, in
  * Products run on the tensor cores with fp32 sums: exp(p) and ds enter as two
  * fp16 values each (hi + lo, 22 bits; exp(p) must stay below 4), x and W as
  * fp16 scaled by a power of two (exact for values down to 2^-32 of the largest
- * finite one).  Every output element is written by one tile: the results are
+ * finite one, to 2^-39 of it below).  Every output element is written by one tile: the results are
  * the same on every run.
  * ws: the size functions' bytes, 256-byte aligned.  dx, dW_r, dW_c, x, W_r,
  * W_c 16-byte aligned.  d % 8 == 0.  Limits: N_r, N_c <= OMNI_MAX_AXIS,
@@ -433,7 +433,7 @@ int omni_layer_norm_bwd(const void *x, const float *mean, const float *rstd, con
  *   nearest even: off by at most 2^-4 of itself, or 2^-10 of the scale near 0.
  *   Infinities and NaN become NaN and do not move the block's scale.
  * pack:   x [L, d] bf16 (fp32 with OMNI_X_F32) -> q [L, d], scale [L, d / 32] bytes
- * unpack: y [L, d] bf16 = value, or value * w + b rounded once (w, b [d] bf16;
+ * unpack (scale bytes up to 254): y [L, d] bf16 = value, or value * w + b rounded once (w, b [d] bf16;
  *         b may be NULL, and w with it): the normed tokens from
  *         omni_layer_norm_fwd's checkpoint
  * d % 32 == 0.  x, q, y, w, b 16-byte aligned.
@@ -447,7 +447,8 @@ int omni_act_unpack(const uint8_t *q, const uint8_t *scale, const omni_bf16 *w,
  * omni_routed_bwd with its tokens taken from a checkpoint:
  * x = omni_act_unpack(q, scale, w, b), then the same arguments and results
  * (dx is the gradient with respect to that x).  The experts and the router
- * see the restored tokens; idx and gate are the forward's.
+ * see the restored tokens; idx and gate are the forward's.  With
+ * OMNI_DW_OVERWRITE the call clears dW, dV, dW_r and dW_c first.
  * ws: omni_routed_bwd_ckpt_workspace_size(...) bytes, 256-byte aligned (the
  * fast path's workspace and the restored tokens, 2 L d bytes).
  */

@@ -48,7 +48,8 @@ def balance_ref(x, W_r, W_c, p_r, p_c, counts, n, K, dloss, mask=None):
     dsr, dsc = c * Pr * (U - tl[:, None]), c * Pc * (V - tl[:, None])
     Ar, Ac = abs(c) * Pr * (U + tl[:, None]), abs(c) * Pc * (V + tl[:, None])
     return dict(loss=fac * tl.sum(), token_loss=tl, dx=dsr @ wr + dsc @ wc, dW_r=dsr.T @ xd,
-                dW_c=dsc.T @ xd, dx_abs=Ar @ wr.abs() + Ac @ wc.abs(), dW_r_abs=Ar.T @ xd.abs(),
+                dW_c=dsc.T @ xd, dx_sum=(Ar.sum(1) + Ac.sum(1))[:, None], dW_r_sum=Ar.sum(0)[:, None],
+                dW_c_sum=Ac.sum(0)[:, None], dx_abs=Ar @ wr.abs() + Ac @ wc.abs(), dW_r_abs=Ar.T @ xd.abs(),
                 dW_c_abs=Ac.T @ xd.abs())
 
 

@@ -5,15 +5,15 @@ norm, 8-bit checkpoints, the routed backward from a checkpoint) against plain
 Tolerances, fixed before the first run.  They are elementwise: a bound on the
 relative error of every term, times the sum of the terms' magnitudes, which the
 reference returns beside the value.
-  balance  ds enters its products as hi + lo bf16 values: what is lost is at
-           most 2^-8 of lo, which is at most 2^-8 of the value: 2^-16.  P
-           enters as hi + lo fp16 values, 2^-22; the same again for the counts
-           and the dropped lo * F_lo when counts pass 2048 (2^-16 is asked for
-           the three, as of the first form of the kernel, whose halves were
-           bf16).  Each fp32 addition in the tensor core loses at most 2^-23 of
-           the running sum of magnitudes; a product over k terms takes 2 k / 16
-           (hi, lo) or 3 k / 16 (F_lo) additions of 16-term sums.  exp and the
-           few other fp32 operations: 2^-20.
+  balance  exp(p) and ds enter their products as two fp16 values, hi + lo: what
+           is lost is at most 2^-11 of lo, which is at most 2^-11 of the value.
+           2^-16 is asked for each (the halves' bound in bf16).  Each fp32
+           addition in the tensor core loses at most 2^-23 of the running sum
+           of magnitudes; a product over k terms takes 2 k / 16 (hi, lo) or
+           3 k / 16 (F_lo) additions of 16-term sums.  exp and the few other
+           fp32 operations: 2^-20.  x and W become fp16 with their largest
+           magnitude at 2^14 at least, where fp16's smallest step is 2^-24:
+           half of it is 2^-39 of the largest, for each value however small.
   norm     y is rounded to bf16 once (2^-8 of itself); the fp32 arithmetic
            before it is off by at most a few units of 2^-24 per operation: mean
            and variance are sums of d terms in chunks of at most 64 and a tree,
@@ -62,7 +62,10 @@ def _within(got, want, tol, what):
 # ---------------------------------------------------------------- counts
 @pytest.mark.parametrize("L,K,N,masked", [(1, 1, 1, False), (1, 5, 7, False), (37, 3, 50, True),
                                           (4096, 16, 4096, True), (1000, 33, 3, False),
-                                          (2048, 64, 1 << 20, False)])
+                                          (2048, 64, 1 << 20, False),
+                                          (16384, 64, 1000, True),       # the crowded table
+                                          (16400, 65, 1 << 20, False),   # ... with few repeats
+                                          (40000, 33, 1, True)])         # ... one expert
 def test_expert_counts(L, K, N, masked):
     g = _gen(L + K)
     idx = torch.randint(0, N, (L, K), generator=g, device=DEV, dtype=torch.int32)
@@ -139,8 +142,11 @@ def _check_balance(x, W_r, W_c, p_r, p_c, idx, mask, K, dloss=0.37, ws_fill=0xff
     got = omni.balance_bwd(x, W_r, W_c, p_r, p_c, cnt["counts"], cnt["n_tokens"], K, fwd["token_loss"],
                            dloss=dloss, mask=mask, ws=ws)
     assert omni.omni_get_device_status(ws) == 0
+    top = {"dx": max(float(W_r.abs().max()), float(W_c.abs().max()))}
+    top["dW_r"] = top["dW_c"] = float((x if mask is None else x[mask]).abs().max())
     for name in ("dx", "dW_r", "dW_c"):
-        _within(got[name], want[name], delta * want[name + "_abs"] + 1e-30, name)
+        tol = delta * want[name + "_abs"] + 2.0 ** -39 * top[name] * want[name + "_sum"] + 1e-30
+        _within(got[name], want[name], tol, name)
         # far inside the worst case, the whole is good to 1e-4, but for what fp32
         # itself leaves where U and l cancel: token_loss is an fp32 output, so
         # its rounding alone moves ds by up to c P l 2^-24, and by linearity the
@@ -168,6 +174,55 @@ def _check_balance(x, W_r, W_c, p_r, p_c, idx, mask, K, dloss=0.37, ws_fill=0xff
 def test_balance(L, d, N_r, N_c, K, masked, hot):
     x, W_r, W_c, p_r, p_c, idx, mask = _balance_inputs(L, d, N_r, N_c, min(K, N_r * N_c), L + d, masked, hot)
     _check_balance(x, W_r, W_c, p_r, p_c, idx, mask, idx.shape[1])
+
+
+@pytest.mark.parametrize("ex,ew", [(60, -50), (-70, 30), (100, 20), (0, -100)])
+def test_balance_scales_of_x_and_w(ex, ew):
+    """Operands far from 1 are scaled by powers of two and back: the same bounds."""
+    x, W_r, W_c, p_r, p_c, idx, _ = _balance_inputs(150, 64, 40, 70, 5, 3)
+    x, W_r, W_c = (t.float() * 2.0 ** e for t, e in ((x, ex), (W_r, ew), (W_c, ew)))
+    x, W_r, W_c = (t.to(torch.bfloat16) for t in (x, W_r, W_c))
+    _check_balance(x, W_r, W_c, p_r, p_c, idx, None, 5)
+
+
+def test_balance_ranges_within_x_and_w():
+    """Columns of x and W from 1 down to 2^-30 of the largest; zero columns;
+    all of x zero; a weight of the loss far from 1."""
+    x, W_r, W_c, p_r, p_c, idx, _ = _balance_inputs(150, 64, 40, 70, 5, 3)
+    s = torch.exp2(-torch.arange(64, device=DEV) * 30.0 / 63).float()
+    x, W_r, W_c = ((t.float() * s).to(torch.bfloat16) for t in (x, W_r, W_c))
+    x[:, 5] = 0
+    W_r[:, 9] = 0
+    _check_balance(x, W_r, W_c, p_r, p_c, idx, None, 5)
+    _check_balance(x, W_r, W_c, p_r, p_c, idx, None, 5, dloss=1e-28)
+    _check_balance(torch.zeros_like(x), W_r, W_c, p_r, p_c, idx, None, 5)
+
+
+def test_balance_offsets_past_32_bits():
+    """L * (N_r + N_c) past 2^31: the last rows, and a weight gradient that only
+    the last rows reach."""
+    L, d, N_r, N_c, K, n = 1_070_000, 8, 1024, 1024, 2, 96
+    g = _gen(5)
+    x = torch.zeros(L, d, dtype=torch.bfloat16, device=DEV)
+    x[-n:] = torch.randn(n, d, generator=g, device=DEV).to(torch.bfloat16)
+    W_r, W_c = (torch.randn(m, d, generator=g, device=DEV).to(torch.bfloat16) for m in (N_r, N_c))
+    p_r, p_c = (torch.full((L, m), -np.log(m), device=DEV) for m in (N_r, N_c))
+    for p in (p_r, p_c):
+        p[-n:] = torch.log_softmax(torch.randn(n, p.shape[1], generator=g, device=DEV), 1)
+    idx = torch.randint(0, N_r * N_c, (L, K), generator=g, device=DEV, dtype=torch.int32)
+    assert L * (N_r + N_c) > 2 ** 31
+    cnt = omni.expert_counts(idx, N_r * N_c)
+    fwd = omni.balance_fwd(p_r, p_c, cnt["counts"], cnt["n_tokens"], K)
+    got = omni.balance_bwd(x, W_r, W_c, p_r, p_c, cnt["counts"], cnt["n_tokens"], K, fwd["token_loss"], dloss=1e6)
+    tail = ref.balance_ref(x[-n:], W_r, W_c, p_r[-n:], p_c[-n:], cnt["counts"], L, K, 1e6 * n / L)
+    one, delta = _delta(N_r, N_c, d, L, False)
+    _within(fwd["token_loss"][-n:], tail["token_loss"], one * tail["token_loss"], "token_loss")
+    # elsewhere p is even: token_loss is the mean count
+    mean = L * K / (N_r * N_c)
+    assert abs(fwd["token_loss"][:-n].double().mean().item() - mean) < 1e-4 * mean
+    _within(got["dx"][-n:], tail["dx"], delta * tail["dx_abs"] + 1e-30, "dx")
+    for k in ("dW_r", "dW_c"):
+        _within(got[k], tail[k], delta * tail[k + "_abs"] + 1e-30, k)
 
 
 def test_balance_against_differences():
@@ -365,6 +420,30 @@ def test_layer_norm_against_differences():
         assert abs(num - (got[name].double() * v).sum()) <= 1e-4 * got[name].double().norm() * v.norm()
 
 
+def test_norm_and_checkpoint_offsets_past_32_bits():
+    """L * d past 2^31: rows at both ends, forward, checkpoint and backward."""
+    L, d = 1_050_000, 2048
+    assert L * d > 2 ** 31
+    x = torch.ones(L, d, dtype=torch.bfloat16, device=DEV)
+    ends = torch.cat([torch.arange(8), torch.arange(L - 8, L)]).to(DEV)
+    sub, w, b, dy = _rows(16, d, torch.bfloat16, 12)
+    x[ends] = sub
+    f = omni.layer_norm_fwd(x, w, b, ckpt=True)
+    want = omni.layer_norm_fwd(sub, w, b, ckpt=True)
+    for k in want:
+        assert torch.equal(f[k][ends], want[k]), k
+    assert torch.equal(f["y"][1000], b)                  # a constant row: xh = 0
+    q, scale = omni.act_pack(x)
+    assert torch.equal(omni.act_unpack(q, scale)[ends], omni.act_unpack(*omni.act_pack(sub)))
+    del x, q, scale
+    big = torch.zeros(L, d, device=DEV)
+    big[ends] = dy
+    g = omni.layer_norm_bwd(big, w, f["rstd"], q=f["q"], scale=f["scale"], dx=big)
+    h = omni.layer_norm_bwd(dy, w, want["rstd"], q=want["q"], scale=want["scale"], dx=dy.clone())
+    assert torch.equal(g["dx"][ends], h["dx"]) and not g["dx"][8:-8].any()
+    _within(g["dw"], h["dw"], 2.0 ** -18 * h["dw"].abs().double() + 2.0 ** -18 * float(dy.abs().max()), "dw")
+
+
 def test_layer_norm_rows_without_spread():
     """Constant rows (xh = 0), rows of zeros, and rows whose mean is far above
     their spread, where a variance from sums of squares would cancel."""
@@ -401,6 +480,32 @@ def test_layer_norm_gradients_accumulate_and_repeat():
     omni.omni_layer_norm_bwd(x, f["mean"], f["rstd"], None, None, w, inplace, L, d, inplace, dw, db,
                              omni.OMNI_X_F32, ws)
     assert torch.equal(inplace, one["dx"]) and torch.equal(dw, one["dw"]) and torch.equal(db, one["db"])
+
+
+def test_overwrite_does_not_read_the_gradients():
+    """OMNI_DW_OVERWRITE on buffers full of NaN, through the C entry points."""
+    L, d, N_r, N_c, K = 70, 256, 20, 30, 4
+    nan = lambda *shape: torch.full(shape, float("nan"), device=DEV)     # noqa: E731
+    x, W_r, W_c, p_r, p_c, idx, _ = _balance_inputs(L, d, N_r, N_c, K, 4)
+    cnt = omni.expert_counts(idx, N_r * N_c)
+    fwd = omni.balance_fwd(p_r, p_c, cnt["counts"], cnt["n_tokens"], K)
+    want = omni.balance_bwd(x, W_r, W_c, p_r, p_c, cnt["counts"], cnt["n_tokens"], K, fwd["token_loss"],
+                            dW_r=torch.zeros(N_r, d, device=DEV))
+    dx, dW_r, dW_c = nan(L, d), nan(N_r, d), nan(N_c, d)
+    ws = torch.empty(omni.omni_balance_bwd_workspace_size(L, d, N_r, N_c), dtype=torch.uint8, device=DEV)
+    omni.omni_balance_bwd(x, W_r, W_c, p_r, p_c, cnt["counts"], cnt["n_tokens"], None, fwd["token_loss"], L, d,
+                          N_r, N_c, K, 1.0, dx, dW_r, dW_c, omni.OMNI_DW_OVERWRITE, ws)
+    for got, k in ((dx, "dx"), (dW_r, "dW_r"), (dW_c, "dW_c")):
+        assert torch.equal(got, want[k]), k
+    r, w, b, dy = _rows(L, d, torch.float32, 9)
+    n = omni.layer_norm_fwd(r, w, b)
+    want = omni.layer_norm_bwd(dy, w, n["rstd"], x=r, mean=n["mean"], dw=torch.zeros(d, device=DEV))
+    dx, dw, db = nan(L, d), nan(d), nan(d)
+    ws = torch.empty(omni.omni_layer_norm_bwd_workspace_size(L, d), dtype=torch.uint8, device=DEV)
+    omni.omni_layer_norm_bwd(r, n["mean"], n["rstd"], None, None, w, dy, L, d, dx, dw, db,
+                             omni.OMNI_X_F32 | omni.OMNI_DW_OVERWRITE, ws)
+    for got, k in ((dx, "dx"), (dw, "dw"), (db, "db")):
+        assert torch.equal(got, want[k]), k
 
 
 # ----------------------------------------------------------- checkpoints
