@@ -436,7 +436,14 @@ constexpr int BM = 128, BN = 256, BK = kSwK, STAGES = 4;     // BM: rows of one 
 constexpr int kBytesA = BM * BK * 2;             // 16 KB, each of hi and lo
 constexpr int kBytesB = BN / 2 * BK * 2;         // 16 KB at most: half of the B tile
 constexpr int kBlockMN = 64 * BK * 2;            // an MN-major box: 64 K rows of 128 bytes
+// All of TMEM: three accumulators for tiles of up to 160 columns, two for wider
+// ones.  An accumulator's way back (its last product to the drained one's
+// arrival) takes about as long as two K steps' products.
 constexpr uint32_t kTmemCols = 2 * BN;
+inline int accumulators(int bn) { return bn <= 160 ? 3 : 2; }
+__device__ __forceinline__ uint32_t acc_column(int accs, int buf) {
+    return (uint32_t)buf * (accs == 3 ? 160u : (uint32_t)BN);
+}
 constexpr int kEpiWarps = 8;                     // two per TMEM lane quarter
 constexpr int kEpiBlocks = BN / 64;              // 32-column blocks of a tile for one of them
 constexpr int kThreads = 32 * (2 + kEpiWarps);
@@ -463,8 +470,8 @@ struct __align__(1024) GemmSmem {
     float turn[kEpiWarps][32 * 32];              // an epilogue warp's 32 x 32 block, between its layouts
     uint64_t full[STAGES];                       // used in the pair's first CTA
     uint64_t empty[STAGES];
-    uint64_t tfull[2];                           // accumulator ready for the epilogue
-    uint64_t tempty[2];                          // accumulator drained (first CTA: both CTAs' warps)
+    uint64_t tfull[3];                           // accumulator ready for the epilogue
+    uint64_t tempty[3];                          // accumulator drained (first CTA: both CTAs' warps)
     uint32_t tmem_base;
     int abort;
 };
@@ -488,6 +495,7 @@ struct GemmProb {
 struct GemmArgs {
     GemmProb prob[kMaxProbs];     // gradients: dW (A is ds^T), then dx
     int nprob, tiles;
+    int accs;                     // accumulators in TMEM
     int ld;                       // columns of ds
     const uint8_t *mask;
     float *part;                  // forward: sums over a tile's columns [tiles_n * 2, L]
@@ -564,7 +572,7 @@ balance_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant
             mbar_init(&sm.full[s], 1);
             mbar_init(&sm.empty[s], 1);
         }
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < 3; ++b) {
             mbar_init(&sm.tfull[b], 1);
             mbar_init(&sm.tempty[b], 2 * kEpiWarps);
         }
@@ -643,7 +651,7 @@ balance_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant
     } else if (warp == 1) {
         if (lane == 0 && rank == 0) {
             // ---- MMA issuer (the pair's first CTA)
-            int it = 0, lt = 0;
+            int it = 0, buf = 0, wrap = 0;
             bool ok = true;
             for (int turn = 0; ok && turns_left(turn, g.tiles); ++turn) {
                 int tile = tile_of(turn, g.tiles);
@@ -657,14 +665,26 @@ balance_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant
                                        (a_mn ? 1u << 15 : 0u) | (MODE == kGrads ? 1u << 16 : 0u);
                 // a 16-deep slice: 32 bytes along a K-major atom, or 16 K rows
                 const uint64_t a_step = (a_mn ? 16 * 128 : 32) >> 4;
-                const uint64_t b_step = (MODE == kGrads ? 16 * 128 : 32) >> 4;
-                for (int st = 0; st < steps; st += kChunk, ++lt) {
-                    if (lt >= 2 &&
-                        !mbar_wait(&sm.tempty[lt & 1], (uint32_t)(((lt >> 1) - 1) & 1), status)) {
+                constexpr uint64_t b_step = (MODE == kGrads ? 16 * 128 : 32) >> 4;
+                const uint64_t a0 = a_mn ? sw128_desc_mn(sm.a[0]) : sw128_desc(sm.a[0]);
+                const uint64_t b0 = MODE == kGrads ? sw128_desc_mn(sm.b[0]) : sw128_desc(sm.b[0]);
+                // one half of A (hi: 0, lo: kBytesA) of stage s times its B
+                const auto products = [&](uint32_t acc, int s, int half, uint32_t started) {
+                    uint64_t ad = a0 + (uint64_t)((s * 2 * kBytesA + half) >> 4);
+                    uint64_t bd = b0 + (uint64_t)((s * kBytesB) >> 4);
+#pragma unroll
+                    for (int k = 0; k < BK / 16; ++k) {
+                        umma_bf16_pair(acc, ad, bd, idesc, k > 0 ? 1u : started);
+                        ad += a_step;
+                        bd += b_step;
+                    }
+                };
+                for (int st = 0; st < steps; st += kChunk) {
+                    if (wrap > 0 && !mbar_wait(&sm.tempty[buf], (uint32_t)((wrap - 1) & 1), status)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t acc = tmem + (uint32_t)((lt & 1) * BN);
+                    const uint32_t acc = tmem + acc_column(g.accs, buf);
                     const int n = min(kChunk, steps - st);
                     uint32_t started = 0;
                     // step i's lo half goes before step i - 1's hi half
@@ -677,33 +697,24 @@ balance_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant
                             }
                             tc_fence_after();
                             if (MODE == kGrads || st + i < p.nk) {    // (hi only times F_lo)
-                                const uint8_t *a = sm.a[s] + kBytesA;
-                                const uint64_t ad = a_mn ? sw128_desc_mn(a) : sw128_desc(a);
-                                const uint64_t bd = MODE == kGrads ? sw128_desc_mn(sm.b[s])
-                                                                   : sw128_desc(sm.b[s]);
-#pragma unroll
-                                for (int k = 0; k < BK / 16; ++k) {
-                                    umma_bf16_pair(acc, ad + k * a_step, bd + k * b_step, idesc, started);
-                                    started = 1;
-                                }
+                                products(acc, s, kBytesA, started);
+                                started = 1;
                             }
                         }
                         if (i > 0) {
                             const int s = (it + i - 1) % STAGES;
-                            const uint64_t ad = a_mn ? sw128_desc_mn(sm.a[s]) : sw128_desc(sm.a[s]);
-                            const uint64_t bd = MODE == kGrads ? sw128_desc_mn(sm.b[s])
-                                                               : sw128_desc(sm.b[s]);
-#pragma unroll
-                            for (int k = 0; k < BK / 16; ++k) {
-                                umma_bf16_pair(acc, ad + k * a_step, bd + k * b_step, idesc, started);
-                                started = 1;
-                            }
+                            products(acc, s, 0, started);
+                            started = 1;
                             umma_commit_pair(&sm.empty[s]);           // frees stage s in both CTAs
                         }
                     }
                     if (!ok) break;
-                    umma_commit_pair(&sm.tfull[lt & 1]);      // both CTAs' epilogues may read
+                    umma_commit_pair(&sm.tfull[buf]);         // both CTAs' epilogues may read
                     it += n;
+                    if (++buf == g.accs) {
+                        buf = 0;
+                        ++wrap;
+                    }
                 }
             }
             if (!ok) sm.abort = 1;
@@ -714,8 +725,7 @@ balance_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant
         // rows of the tile) and every second block of 32 columns
         const int quarter = warp & 3;
         const int half = (warp - 2) >> 2;
-        const uint32_t tempty0 = smem_in_cta(&sm.tempty[0], 0);
-        const uint32_t tempty1 = smem_in_cta(&sm.tempty[1], 0);
+        const uint32_t tempty = smem_in_cta(&sm.tempty[0], 0);
         float *turn_buf = sm.turn[warp - 2];
         // kGrid: ds / c to below 2^15, and P's 2^14 out; kGrads: that scale out,
         // the operand's (scale2), and c in
@@ -726,7 +736,7 @@ balance_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant
             if (n > 0 && kept > 0) coef = g.factor / (float)n / (float)kept;
             scale1 = pow2f(count_exp(g.hdr->most) - 15);
         }
-        int lt = 0;
+        int buf = 0, wrap = 0;
         bool ok = true;
         for (int turn = 0; ok && turns_left(turn, g.tiles); ++turn) {
             int tile = tile_of(turn, g.tiles);
@@ -759,15 +769,15 @@ balance_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant
             for (int q = 0; q < kEpiBlocks; ++q)
 #pragma unroll
                 for (int j = 0; j < 32; ++j) sum[q][j] = 0.f;
-            for (int st = 0; st < steps; st += kChunk, ++lt) {
+            for (int st = 0; st < steps; st += kChunk) {
                 // the warp gives up as one: its lanes meet again below
-                const bool got = mbar_wait(&sm.tfull[lt & 1], (uint32_t)((lt >> 1) & 1), status);
+                const bool got = mbar_wait(&sm.tfull[buf], (uint32_t)(wrap & 1), status);
                 if (!__all_sync(0xffffffffu, got)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t tb = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)((lt & 1) * BN);
+                const uint32_t tb = tmem + ((uint32_t)(quarter * 32) << 16) + acc_column(g.accs, buf);
 #pragma unroll
                 for (int q = 0; q < kEpiBlocks; ++q) {
                     if (half + 2 * q < blocks) {
@@ -784,7 +794,11 @@ balance_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant
                 // both CTAs is done (the first CTA's barrier counts all 16)
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_pair((lt & 1) ? tempty1 : tempty0);
+                if (lane == 0) mbar_arrive_pair(tempty + 8u * (uint32_t)buf);
+                if (++buf == g.accs) {
+                    buf = 0;
+                    ++wrap;
+                }
             }
             if (!ok) break;
             // a masked row has P = 0, its sums are finite and its token_loss is not used
@@ -998,12 +1012,13 @@ void set_tiles(GemmProb *p, int cols, int bn) {
 }
 
 template <int MODE>
-cudaError_t launch_gemm(const GemmMaps &maps, const GemmArgs &g, cudaStream_t st) {
+cudaError_t launch_gemm(const GemmMaps &maps, GemmArgs &g, cudaStream_t st) {
     const int smem = (int)sizeof(GemmSmem) + 1024;
     const cudaError_t e = cudaFuncSetAttribute(balance_gemm_kernel<MODE>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int most = device_sm_count() / 2, pairs = g.tiles < most ? g.tiles : most;
+    g.accs = accumulators(g.prob[0].bn);         // a launch's problems share their tile width
     return launch(balance_gemm_kernel<MODE>, dim3((unsigned)(2 * pairs)), dim3(kThreads),
                   (size_t)smem, st, maps, g);
 }
