@@ -843,29 +843,30 @@ balance_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant
                     __syncwarp();
                 }
                 if constexpr (MODE == kGrid) {
-                    // four rows at a time, four columns to a lane; P as the operand holds it
-                    const int c = 4 * ((int)lane & 7), r0 = (int)lane >> 3;
+                    // eight rows at a time, eight columns to a lane; P as the operand holds it
+                    const int c = 8 * ((int)lane & 3), r0 = (int)lane >> 2;
                     const int64_t at = (int64_t)(row0 + r0) * g.ld + col0 + c;
 #pragma unroll 1
-                    for (int i4 = 0; i4 < 8; i4 += 4) {
-                        uint2 hi[4], lo[4];
+                    for (int i2 = 0; i2 < 4; i2 += 2) {
+                        uint4 hi[2], lo[2];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int64_t o = at + 4 * (i4 + i) * g.ld;
-                            const bool in = row0 + r0 + 4 * (i4 + i) < p.M;
-                            hi[i] = in ? __ldg(reinterpret_cast<const uint2 *>(p.P_hi + o)) : make_uint2(0, 0);
-                            lo[i] = in ? __ldg(reinterpret_cast<const uint2 *>(p.P_lo + o)) : make_uint2(0, 0);
+                        for (int i = 0; i < 2; ++i) {
+                            const int64_t o = at + 8 * (i2 + i) * g.ld;
+                            const bool in = row0 + r0 + 8 * (i2 + i) < p.M;
+                            hi[i] = in ? __ldg(reinterpret_cast<const uint4 *>(p.P_hi + o)) : make_uint4(0, 0, 0, 0);
+                            lo[i] = in ? __ldg(reinterpret_cast<const uint4 *>(p.P_lo + o)) : make_uint4(0, 0, 0, 0);
                         }
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int r = r0 + 4 * (i4 + i);
+                        for (int i = 0; i < 2; ++i) {
+                            const int r = r0 + 8 * (i2 + i);
                             const float l = __shfl_sync(0xffffffffu, l_t, r);
-                            uint32_t oh[2], ol[2];
+                            const uint4 h4 = hi[i], l4 = lo[i];
+                            const uint32_t wh[4] = {h4.x, h4.y, h4.z, h4.w}, wl[4] = {l4.x, l4.y, l4.z, l4.w};
+                            uint32_t oh[4], ol[4];
 #pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                const uint32_t wh = k ? hi[i].y : hi[i].x, wl = k ? lo[i].y : lo[i].x;
-                                const float2 ph = __half22float2(*reinterpret_cast<const __half2 *>(&wh));
-                                const float2 pl = __half22float2(*reinterpret_cast<const __half2 *>(&wl));
+                            for (int k = 0; k < 4; ++k) {
+                                const float2 ph = __half22float2(*reinterpret_cast<const __half2 *>(&wh[k]));
+                                const float2 pl = __half22float2(*reinterpret_cast<const __half2 *>(&wl[k]));
                                 const float a = (ph.x + pl.x) * scale1 *
                                                 (kUnscale * turn_buf[turned(r, c + 2 * k)] - l);
                                 const float b = (ph.y + pl.y) * scale1 *
@@ -877,9 +878,9 @@ balance_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant
                                 ol[k] = *reinterpret_cast<const uint32_t *>(&o);
                             }
                             if (row0 + r < p.M) {
-                                const int64_t o = at + 4 * (i4 + i) * g.ld;
-                                *reinterpret_cast<uint2 *>(p.ds_hi + o) = make_uint2(oh[0], oh[1]);
-                                *reinterpret_cast<uint2 *>(p.ds_lo + o) = make_uint2(ol[0], ol[1]);
+                                const int64_t o = at + 8 * (i2 + i) * g.ld;
+                                *reinterpret_cast<uint4 *>(p.ds_hi + o) = make_uint4(oh[0], oh[1], oh[2], oh[3]);
+                                *reinterpret_cast<uint4 *>(p.ds_lo + o) = make_uint4(ol[0], ol[1], ol[2], ol[3]);
                             }
                         }
                     }
