@@ -31,15 +31,15 @@
 //     2^15.  fp16 then holds every bf16 value down to 2^-32 of it exactly.
 // bf16 halves (16 bits) need no scales, but left dx and dW off by 2.9e-6 of
 // themselves, and by 4e-3 for a collapsed router, where U - l_t cancels.  With
-// these, and with what chunk_steps below says, the results are as near to 64 bits
-// as fp32 arithmetic's (headline: 6e-7, torch in fp32 1.2e-6).
+// these, and with what kChunk below says, the results are as near to 64 bits
+// as fp32 arithmetic's (headline: 5e-7, torch in fp32 1.2e-6).
 //
 // Bounds and measurements, headline layer (L = 4096, d = 1024, 1304 x 1304
 // grid, one B200, clocks under load): the products are 28 GFLOP forward, 56 +
 // 87 GFLOP backward, twice the definition's because of the halves, against
-// 1407 TFLOP/s sustained.  Forward 42 us (20 at that rate), U and V with ds 80
-// us (40), dW and dx 85 us (62).  What is above goes to handing accumulators
-// over every second or third K step (21 us less in all at every fourth), to
+// 1407 TFLOP/s sustained.  Forward 42 us (20 at that rate), U and V with ds 76
+// us (40), dW and dx 91 us (62).  What is above goes to handing accumulators
+// over every second K step (18 us less in all at every fourth), to
 // the rounds that do not fill 74 pairs (192 tiles of 256 x 224; 44 tiles of 64
 // and 64 of 42 K steps), and in U and V to the 88 MB of P and ds that the
 // epilogue reads and writes.  Preparing the operands takes 41 us for the two
@@ -454,15 +454,12 @@ constexpr int kMaxProbs = 2, kMaxMaps = 6;
 // registers.  The tensor core cuts off what falls below its accumulator at
 // every instruction, always towards zero: over the 512 instructions of a dW
 // tile at L = 4096 that took 1.1e-5 off the result, and it grows with L.  Here
-// an accumulator takes two steps of U and V (8 + 8 instructions, the lo halves
-// first, while it is small) or three of dW and dx (each step's lo half before
-// the hi half of the step before it); the additions in registers round to
-// nearest.  U and l_t cancel and l_t is an output, so they get the shorter
-// sums.  Headline step and largest error against 64 bits at the headline, and
-// at the skewed layer: 2 and 3 steps 266 us, 6e-7, 1.4e-6; 4 steps 248 us,
-// 7e-7, 2.9e-6; 8 steps, halves together, 227 us, 2e-6, 5.6e-6 (torch in fp32:
-// 1.2e-6 and 2.7e-6).
-__host__ __device__ constexpr int chunk_steps(int mode) { return mode == 2 ? 3 : 2; }   // 2: kGrads
+// an accumulator takes the 8 instructions of two lo halves first, while it is
+// small, then the 8 of the hi halves; the additions in registers round to
+// nearest.  Headline step, and largest error against 64 bits there and at the
+// skewed layer: 2 steps 266 us, 5e-7, 1.3e-6; 4 steps 248 us, 7e-7, 2.9e-6; 8
+// steps, halves together, 227 us, 2e-6, 5.6e-6 (torch in fp32: 1.2e-6, 2.7e-6).
+constexpr int kChunk = 2;
 
 struct __align__(1024) GemmSmem {
     uint8_t a[STAGES][2 * kBytesA];
@@ -565,7 +562,6 @@ balance_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant
     const unsigned lane = lane_id();
     const uint32_t rank = cluster_ctarank();         // 0: issues the MMAs
     int *status = &g.hdr->status;
-    constexpr int kChunk = chunk_steps(MODE);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
