@@ -198,7 +198,7 @@ int reset_workspace(void *ws, const WsLayout &lay, cudaStream_t st) {
 // Grid sizes of the balance calls (K only scales them).
 int check_grid(int L, int N_r, int N_c, int K) {
     if (L <= 0 || N_r <= 0 || N_c <= 0 || K <= 0) return OMNI_ERR_INVALID_ARG;
-    if (N_r > OMNI_MAX_AXIS || N_c > OMNI_MAX_AXIS) return OMNI_ERR_UNSUPPORTED;
+    if (N_r > OMNI_MAX_AXIS || N_c > OMNI_MAX_AXIS || L > (1 << 30)) return OMNI_ERR_UNSUPPORTED;
     return OMNI_OK;
 }
 

@@ -436,9 +436,8 @@ constexpr int BM = 128, BN = 256, BK = kSwK, STAGES = 4;     // BM: rows of one 
 constexpr int kBytesA = BM * BK * 2;             // 16 KB, each of hi and lo
 constexpr int kBytesB = BN / 2 * BK * 2;         // 16 KB at most: half of the B tile
 constexpr int kBlockMN = 64 * BK * 2;            // an MN-major box: 64 K rows of 128 bytes
-// All of TMEM: three accumulators for tiles of up to 160 columns, two for wider
-// ones.  An accumulator's way back (its last product to the drained one's
-// arrival) takes about as long as two K steps' products.
+// All of TMEM: three accumulators for tiles of up to 160 columns (forward at the
+// headline: 41.7 us, with two 43.1), two for wider ones.
 constexpr uint32_t kTmemCols = 2 * BN;
 inline int accumulators(int bn) { return bn <= 160 ? 3 : 2; }
 __device__ __forceinline__ uint32_t acc_column(int accs, int buf) {
@@ -477,6 +476,7 @@ struct GemmProb {
     int M, N;                     // rows and columns of C
     int bn, tiles_n, tiles;       // tile width, tiles in N, tiles in all
     int nk;                       // 64-element steps of the K axis
+    int a_mn;                     // A is MN-major (ds^T, for dW)
     int a_hi, a_lo;               // tensor maps of A
     int a_c0;                     // first column of A's segment in its matrix
     int b, b_lo;                  // maps of B, and of the remainder F_lo
@@ -490,7 +490,7 @@ struct GemmProb {
 };
 
 struct GemmArgs {
-    GemmProb prob[kMaxProbs];     // gradients: dW (A is ds^T), then dx
+    GemmProb prob[kMaxProbs];     // the one with the longer K axis first
     int nprob, tiles;
     int accs;                     // accumulators in TMEM
     int ld;                       // columns of ds
@@ -596,12 +596,11 @@ balance_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant
             for (int turn = 0; !sm.abort && turns_left(turn, g.tiles); ++turn) {
                 int tile = tile_of(turn, g.tiles);
                 if (tile < 0) continue;
-                const int pk = find_prob(g, &tile);
-                const GemmProb &p = g.prob[pk];
+                const GemmProb &p = g.prob[find_prob(g, &tile)];
                 const int m0 = (tile / p.tiles_n) * 2 * BM + (int)rank * BM;
                 const int n0 = (tile % p.tiles_n) * p.bn + (int)rank * (p.bn / 2);
                 const int steps = steps_of<MODE>(p, big);
-                const bool a_mn = MODE == kGrads && pk == 0;             // dW: A is ds^T
+                const bool a_mn = MODE == kGrads && p.a_mn;
                 for (int st = 0; st < steps; ++st, ++it) {
                     const int s = it % STAGES;
                     if (it >= STAGES &&
@@ -652,10 +651,9 @@ balance_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant
             for (int turn = 0; ok && turns_left(turn, g.tiles); ++turn) {
                 int tile = tile_of(turn, g.tiles);
                 if (tile < 0) continue;
-                const int pk = find_prob(g, &tile);
-                const GemmProb &p = g.prob[pk];
+                const GemmProb &p = g.prob[find_prob(g, &tile)];
                 const int steps = steps_of<MODE>(p, big);
-                const bool a_mn = MODE == kGrads && pk == 0;
+                const bool a_mn = MODE == kGrads && p.a_mn;
                 // bits 15 and 16 of the instruction descriptor: A, B are MN-major
                 const uint32_t idesc = kIdescF16 | ((uint32_t)(p.bn >> 3) << 17) |
                                        (a_mn ? 1u << 15 : 0u) | (MODE == kGrads ? 1u << 16 : 0u);
@@ -737,8 +735,7 @@ balance_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant
         for (int turn = 0; ok && turns_left(turn, g.tiles); ++turn) {
             int tile = tile_of(turn, g.tiles);
             if (tile < 0) continue;
-            const int pk = find_prob(g, &tile);
-            const GemmProb &p = g.prob[pk];
+            const GemmProb &p = g.prob[find_prob(g, &tile)];
             const int row0 = (tile / p.tiles_n) * 2 * BM + (int)rank * BM + quarter * 32;
             const int tn = tile % p.tiles_n, n0 = tn * p.bn;
             const int steps = steps_of<MODE>(p, big), blocks = p.bn / 32;
@@ -801,7 +798,7 @@ balance_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant
             const bool keep = MODE != kGrads && row < p.M && (!g.mask || g.mask[row]);
             const bool vec = MODE == kFwd && float4_rows(p.p, p.N);
             const float l_t = MODE == kGrid && keep ? g.token_loss[row] : 0.f;
-            if (MODE == kGrads) scale2 = pow2f(-top_exp(pk == 0 ? g.hdr->x_top : g.hdr->w_top));
+            if (MODE == kGrads) scale2 = pow2f(-top_exp(p.a_mn ? g.hdr->x_top : g.hdr->w_top));
             float part = 0.f;
 #pragma unroll
             for (int q = 0; q < kEpiBlocks; ++q) {
@@ -1156,11 +1153,14 @@ cudaError_t launch_balance_bwd(const uint16_t *x, const uint16_t *W_r, const uin
     GemmArgs g = {};
     g.mask = mask; g.token_loss = token_loss; g.hdr = pp.hdr; g.ld = w.ld;
     g.nprob = 2;
-    // the pad columns belong to the tiles too: they must be written as zeros
+    // the pad columns belong to the tiles too: they must be written as zeros.
+    // U's products run over the columns and V's over the rows
     const int segs[2] = {pp.pr, pp.pc};
     const int bn = pick_width(segs, 2, mtiles, device_sm_count() / 2);
-    for (int a = 0; a < 2; ++a) {                    // U with ds_r, V with ds_c
-        GemmProb &p = g.prob[a];
+    const int longer = segs[1] >= segs[0] ? 0 : 1;
+    for (int k = 0; k < 2; ++k) {
+        const int a = k ^ longer;                    // 0: U with ds_r, 1: V with ds_c
+        GemmProb &p = g.prob[k];
         p.M = L; p.N = a == 0 ? N_r : N_c;
         p.nk = segs[1 - a] / BK;
         p.a_hi = 0; p.a_lo = 1; p.a_c0 = a == 0 ? pp.pr : 0;
@@ -1187,13 +1187,14 @@ cudaError_t launch_balance_bwd(const uint16_t *x, const uint16_t *W_r, const uin
     h.hdr = pp.hdr; h.n_tokens = n_tokens;
     h.factor = (float)((double)dloss * N_r * N_c / K);
     h.nprob = 2;
-    GemmProb &dw = h.prob[0];                        // A is ds^T, K the tokens
-    dw.M = w.ld; dw.N = d; dw.nk = (L + BK - 1) / BK;
+    const int nk_dw = (L + BK - 1) / BK, nk_dx = w.ld / BK;
+    GemmProb &dw = h.prob[nk_dw < nk_dx];            // A is ds^T, K the tokens
+    dw.M = w.ld; dw.N = d; dw.nk = nk_dw; dw.a_mn = 1;
     dw.a_hi = 2; dw.a_lo = 3; dw.b = 4;
     dw.out = dW_r; dw.out2 = dW_c; dw.split = pp.pr; dw.rows1 = N_r; dw.rows2 = N_c;
     dw.accumulate = overwrite ? 0 : 1;
-    GemmProb &px = h.prob[1];
-    px.M = L; px.N = d; px.nk = w.ld / BK;
+    GemmProb &px = h.prob[nk_dw >= nk_dx];
+    px.M = L; px.N = d; px.nk = nk_dx;
     px.a_hi = 0; px.a_lo = 1; px.b = 5;
     px.out = dx; px.split = L; px.rows1 = L;
     px.accumulate = accumulate ? 1 : 0;

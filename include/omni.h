@@ -373,7 +373,7 @@ int omni_expert_counts(const int32_t *idx, const uint8_t *mask, int L, int K, in
  * the same on every run.
  * ws: the size functions' bytes, 256-byte aligned.  dx, dW_r, dW_c, x, W_r,
  * W_c 16-byte aligned.  d % 8 == 0.  Limits: N_r, N_c <= OMNI_MAX_AXIS,
- * N < 2^31.
+ * L <= 2^30.
  */
 size_t omni_balance_fwd_workspace_size(int L, int N_r, int N_c);
 int omni_balance_fwd(const float *p_r, const float *p_c, const int32_t *counts,

@@ -142,14 +142,14 @@ def test_balance_refusals(lib):
     ok = [FAKE, FAKE, FAKE, FAKE, None, 4, 8, 8, 2, FAKE, FAKE, FAKE, BIG, None]
     _try_all_pointers(lib.omni_balance_fwd, ok, (0, 1, 2, 3, 9, 10, 11))
     for at, v, rc in ((5, 0, -1), (6, 0, -1), (7, -1, -1), (8, 0, -1), (6, 8193, -2), (7, 8193, -2),
-                      (12, 1000, -3), (0, ODD, -1), (11, _p((1 << 20) + 16), -1)):
+                      (12, 1000, -3), (0, ODD, -1), (11, _p((1 << 20) + 16), -1), (5, (1 << 30) + 1, -2)):
         bad = list(ok)
         bad[at] = v
         assert lib.omni_balance_fwd(*bad) == rc, (at, v)
     ok = [FAKE] * 7 + [None, FAKE, 4, 64, 8, 8, 2, 1.0, FAKE, FAKE, FAKE, 0, FAKE, BIG, None]
     _try_all_pointers(lib.omni_balance_bwd, ok, (0, 1, 2, 3, 4, 5, 6, 8, 15, 16, 17, 19))
     for at, v, rc in ((9, 0, -1), (10, 0, -1), (10, 12, -2), (11, 9000, -2), (13, 0, -1), (18, 1, -1),
-                      (20, 1000, -3), (0, ODD, -1), (15, _p((1 << 20) + 4), -1), (3, ODD, -1)):
+                      (20, 1000, -3), (0, ODD, -1), (15, _p((1 << 20) + 4), -1), (3, ODD, -1), (9, (1 << 30) + 1, -2)):
         bad = list(ok)
         bad[at] = v
         assert lib.omni_balance_bwd(*bad) == rc, (at, v)
