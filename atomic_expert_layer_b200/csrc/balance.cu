@@ -978,19 +978,24 @@ balance_loss_kernel(const float *__restrict__ part, int nparts, int L, float *__
 
 inline int pad64(int n) { return (n + 63) / 64 * 64; }
 
+// Clocks of a K step of a tile bn columns wide: its 8 MMAs take 4 per column;
+// its shared-memory traffic (operands read and filled) is 64 KB and 192 bytes
+// per column at 128 bytes a clock, which is more for narrow tiles.
+inline int step_clocks(int bn) {
+    const int mma = 4 * bn, smem = 512 + bn * 3 / 2;
+    return mma > smem ? mma : smem;
+}
+
 // Width of the tiles of a launch whose problems have n[i] columns and as many
 // 256-row tiles: the one that takes the least time in whole rounds of the
-// pairs.  A K step's 8 MMAs take 4 clocks per column; its shared-memory
-// traffic (operands read and filled) is 64 KB and 192 bytes per column at 128
-// bytes a clock, which is more for narrow tiles.
+// pairs.
 int pick_width(const int *n, int probs, int mtiles, int pairs) {
     int best = 0;
     int64_t best_cost = 0;
     for (int bn = BN; bn >= 64; bn -= 32) {
         int64_t tiles = 0;
         for (int i = 0; i < probs; ++i) tiles += (int64_t)mtiles * ((n[i] + bn - 1) / bn);
-        const int mma = 4 * bn, smem = 512 + bn * 3 / 2;
-        const int64_t cost = (tiles + pairs - 1) / pairs * (mma > smem ? mma : smem);
+        const int64_t cost = (tiles + pairs - 1) / pairs * step_clocks(bn);
         if (best == 0 || cost < best_cost) {
             best = bn;
             best_cost = cost;
@@ -1005,6 +1010,28 @@ void set_tiles(GemmProb *p, int cols, int bn) {
     p->tiles = ((p->M + 2 * BM - 1) / (2 * BM)) * p->tiles_n;
 }
 
+// Widths of dW's and dx's tiles, 128 or 256 (whole 64-element boxes in each
+// CTA): 256, unless narrower ones of one of them or both still make one round
+// of the pairs and a shorter one.
+void set_grad_tiles(GemmProb *p, int d, int pairs) {
+    int64_t best = 0;
+    int width[2] = {256, 256};
+    for (int k = 0; k < 4; ++k) {
+        const int w[2] = {k & 1 ? 128 : 256, k & 2 ? 128 : 256};
+        set_tiles(&p[0], d, w[0]);
+        set_tiles(&p[1], d, w[1]);
+        const int64_t a = (int64_t)p[0].nk * step_clocks(w[0]), b = (int64_t)p[1].nk * step_clocks(w[1]);
+        const int64_t cost = a > b ? a : b;
+        if (k == 0 || ((int64_t)p[0].tiles + p[1].tiles <= pairs && cost < best)) {
+            best = cost;
+            width[0] = w[0];
+            width[1] = w[1];
+        }
+    }
+    set_tiles(&p[0], d, width[0]);
+    set_tiles(&p[1], d, width[1]);
+}
+
 template <int MODE>
 cudaError_t launch_gemm(const GemmMaps &maps, GemmArgs &g, cudaStream_t st) {
     const int smem = (int)sizeof(GemmSmem) + 1024;
@@ -1012,7 +1039,9 @@ cudaError_t launch_gemm(const GemmMaps &maps, GemmArgs &g, cudaStream_t st) {
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int most = device_sm_count() / 2, pairs = g.tiles < most ? g.tiles : most;
-    g.accs = accumulators(g.prob[0].bn);         // a launch's problems share their tile width
+    int bn = 0;
+    for (int k = 0; k < g.nprob; ++k) bn = g.prob[k].bn > bn ? g.prob[k].bn : bn;
+    g.accs = accumulators(bn);
     return launch(balance_gemm_kernel<MODE>, dim3((unsigned)(2 * pairs)), dim3(kThreads),
                   (size_t)smem, st, maps, g);
 }
@@ -1198,9 +1227,7 @@ cudaError_t launch_balance_bwd(const uint16_t *x, const uint16_t *W_r, const uin
     px.a_hi = 0; px.a_lo = 1; px.b = 5;
     px.out = dx; px.split = L; px.rows1 = L;
     px.accumulate = accumulate ? 1 : 0;
-    const int bg = d > 128 ? 256 : 128;              // MN-major: whole 64-element boxes in each CTA
-    set_tiles(&dw, d, bg);
-    set_tiles(&px, d, bg);
+    set_grad_tiles(h.prob, d, device_sm_count() / 2);
     h.tiles = dw.tiles + px.tiles;
     if (!make_sw128_map(&maps.m[0], ds_hi, L, w.ld, BM) ||
         !make_sw128_map(&maps.m[1], ds_lo, L, w.ld, BM) ||
