@@ -458,7 +458,11 @@ constexpr int kMaxProbs = 2, kMaxMaps = 6;
 // nearest.  Headline step, and largest error against 64 bits there and at the
 // skewed layer: 2 steps 266 us, 5e-7, 1.3e-6; 4 steps 248 us, 7e-7, 2.9e-6; 8
 // steps, halves together, 227 us, 2e-6, 5.6e-6 (torch in fp32: 1.2e-6, 2.7e-6).
-constexpr int kChunk = 2;
+// A backward tile's first two accumulators take up to kMaxLead steps (a fifth
+// of them at most): they are computed while the warps that would drain them
+// still write the last tile (headline step 265 -> 258 us; with 8 steps and a
+// quarter 250, but 2e-6 at the skewed layer).
+constexpr int kChunk = 2, kMaxLead = 4;
 
 struct __align__(1024) GemmSmem {
     uint8_t a[STAGES][2 * kBytesA];
@@ -476,6 +480,7 @@ struct GemmProb {
     int M, N;                     // rows and columns of C
     int bn, tiles_n, tiles;       // tile width, tiles in N, tiles in all
     int nk;                       // 64-element steps of the K axis
+    int lead;                     // steps of a tile's first two accumulators
     int a_mn;                     // A is MN-major (ds^T, for dW)
     int a_hi, a_lo;               // tensor maps of A
     int a_c0;                     // first column of A's segment in its matrix
@@ -534,6 +539,13 @@ __device__ __forceinline__ uint64_t sw128_desc_mn(const void *tile) {
 template <int MODE>
 __device__ __forceinline__ int steps_of(const GemmProb &p, bool big) {
     return MODE != kGrads && big ? 2 * p.nk : p.nk;
+}
+
+// K steps of the accumulator that begins at step st.
+template <int MODE>
+__device__ __forceinline__ int chunk_steps(const GemmProb &p, int st, int steps) {
+    const int n = MODE != kFwd && st < 2 * p.lead ? p.lead : kChunk;
+    return min(n, steps - st);
 }
 
 // Arrive on the pair's first CTA's barrier.  What it orders are TMEM reads,
@@ -673,13 +685,13 @@ balance_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant
                         bd += b_step;
                     }
                 };
-                for (int st = 0; st < steps; st += kChunk) {
+                for (int st = 0, n; st < steps; st += n) {
+                    n = chunk_steps<MODE>(p, st, steps);
                     if (wrap > 0 && !mbar_wait(&sm.tempty[buf], (uint32_t)((wrap - 1) & 1), status)) {
                         ok = false;
                         break;
                     }
                     const uint32_t acc = tmem + acc_column(g.accs, buf);
-                    const int n = min(kChunk, steps - st);
                     uint32_t started = 0;
                     // step i's lo half goes before step i - 1's hi half
                     for (int i = 0; i <= n; ++i) {
@@ -762,7 +774,7 @@ balance_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant
             for (int q = 0; q < kEpiBlocks; ++q)
 #pragma unroll
                 for (int j = 0; j < 32; ++j) sum[q][j] = 0.f;
-            for (int st = 0; st < steps; st += kChunk) {
+            for (int st = 0; st < steps; st += chunk_steps<MODE>(p, st, steps)) {
                 // the warp gives up as one: its lanes meet again below
                 const bool got = mbar_wait(&sm.tfull[buf], (uint32_t)(wrap & 1), status);
                 if (!__all_sync(0xffffffffu, got)) {
@@ -1005,6 +1017,8 @@ int pick_width(const int *n, int probs, int mtiles, int pairs) {
 }
 
 void set_tiles(GemmProb *p, int cols, int bn) {
+    const int fifth = p->nk / 5;
+    p->lead = fifth < kChunk ? kChunk : fifth > kMaxLead ? kMaxLead : fifth;
     p->bn = bn;
     p->tiles_n = (cols + bn - 1) / bn;
     p->tiles = ((p->M + 2 * BM - 1) / (2 * BM)) * p->tiles_n;

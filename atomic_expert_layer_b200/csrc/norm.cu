@@ -260,7 +260,7 @@ norm_fwd_kernel(const T *__restrict__ x, const uint16_t *__restrict__ w,
             }
         }
         sum(s, group);
-        const float rstd = rsqrtf(fmaf(s[0], inv_d, eps));
+        const float rstd = __frsqrt_rn(fmaf(s[0], inv_d, eps));
         if (c == 0) {
             if (mean_out) mean_out[row] = mean;
             if (rstd_out) rstd_out[row] = rstd;
