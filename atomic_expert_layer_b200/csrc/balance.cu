@@ -37,13 +37,12 @@
 // Bounds and measurements, headline layer (L = 4096, d = 1024, 1304 x 1304
 // grid, one B200, clocks under load): the products are 28 GFLOP forward, 56 +
 // 87 GFLOP backward, twice the definition's because of the halves, against
-// 1407 TFLOP/s sustained.  Forward 42 us (20 at that rate), U and V with ds 76
-// us (40), dW and dx 91 us (62).  What is above goes to handing accumulators
-// over every second K step (18 us less in all at every fourth), to
-// the rounds that do not fill 74 pairs (192 tiles of 256 x 224; 44 tiles of 64
-// and 64 of 42 K steps), and in U and V to the 88 MB of P and ds that the
-// epilogue reads and writes.  Preparing the operands takes 41 us for the two
-// calls (173 MB).
+// 1407 TFLOP/s sustained.  Forward 41 us (20 at that rate), U and V with ds 71
+// us (40), dW and dx 87 us (62).  What is above goes to the tiles' output,
+// which two accumulators do not cover (U and V without it: 48 us), to handing
+// accumulators over every second K step, to the rounds that do not fill 74
+// pairs (192 tiles of 256 x 224; 44 tiles of 64 and 64 of 42 K steps).
+// Preparing the operands takes 41 us for the two calls (173 MB).
 //
 // Masked rows of p are never read as numbers: their P and ds are zero.
 #include <cuda_fp16.h>
