@@ -190,32 +190,39 @@ struct BalPrep {
     BalHeader *hdr;
 };
 
-// 8 log-probabilities from column col on (those past n: none), as fast as the
-// row's alignment allows.
-__device__ __forceinline__ void load_logp8(const float *row, int col, int n, bool vec, float *v) {
-    if (vec && col + 8 <= n) {
-        const float4 a = reinterpret_cast<const float4 *>(row + col)[0];
-        const float4 b = reinterpret_cast<const float4 *>(row + col)[1];
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    } else {
+// 8 log-probabilities from `at` on, of which `valid` exist (the others read as
+// -inf).  A row starts at any multiple of 4 bytes, so they come as the 2 or 3
+// aligned 16-byte chunks that hold at least one of them (what else a chunk holds
+// lies beside it in memory and is dropped), shifted into place.  At 6001 tokens
+// and 1101 x 1303 the U product takes 47 us so (58 with 4-byte loads) and the
+// preparation 50 (58); at 4096 tokens and 1304 x 1304 they take 40 and 42 us (41
+// and 42 with a branch of its own for aligned rows).
+__device__ __forceinline__ void load_logp8(const float *at, int valid, float *v) {
+    const int m = (int)(reinterpret_cast<uintptr_t>(at) >> 2) & 3;
+    const float4 *chunk = reinterpret_cast<const float4 *>(at - m);
+    float w[12];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = col + i < n ? row[col + i] : -INFINITY;
+    for (int k = 0; k < 3; ++k) {
+        float4 c = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (4 * k - m < valid && (k < 2 || m > 0)) c = __ldg(chunk + k);
+        w[4 * k] = c.x, w[4 * k + 1] = c.y, w[4 * k + 2] = c.z, w[4 * k + 3] = c.w;
     }
-}
-__device__ __forceinline__ bool float4_rows(const float *p, int n) {
-    return (n & 3) == 0 && (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        v[i] = m < 2 ? (m == 0 ? w[i] : w[i + 1]) : (m == 2 ? w[i + 2] : w[i + 3]);
+        if (i >= valid) v[i] = -INFINITY;
+    }
 }
 
 // A warp's 256 columns of a row of P: both segments, the padding as zeros.
-__device__ __forceinline__ void prep_probs(const BalPrep &p, int64_t t, int c0, bool vec_r, bool vec_c) {
+__device__ __forceinline__ void prep_probs(const BalPrep &p, int64_t t, int c0) {
     c0 += 8 * (int)lane_id();
     if (c0 >= p.ld) return;
     float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (!p.mask || p.mask[t]) {
         const bool rows = c0 < p.seg_r;
-        load_logp8(rows ? p.p_r + t * p.N_r : p.p_c + t * p.N_c, rows ? c0 : c0 - p.seg_r,
-                   rows ? p.N_r : p.N_c, rows ? vec_r : vec_c, v);
+        const int col = rows ? c0 : c0 - p.seg_r, n = rows ? p.N_r : p.N_c;
+        load_logp8((rows ? p.p_r + t * p.N_r : p.p_c + t * p.N_c) + col, n - col, v);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = kScaleP * expf(v[i]);
     }
@@ -342,9 +349,8 @@ __global__ void __launch_bounds__(kPrepThreads, kPrepPerSm) balance_prep_kernel(
     // one warp per 256 columns of a row from here on
     const int64_t warps = (int64_t)gridDim.x * (kPrepThreads / 32);
     const int64_t w0 = (int64_t)blockIdx.x * (kPrepThreads / 32) + (threadIdx.x >> 5);
-    const bool vec_r = float4_rows(p.p_r, p.N_r), vec_c = float4_rows(p.p_c, p.N_c);
     for (Pieces u(w0, warps, (p.ld + 255) / 256); u.row < p.L; u.next())
-        prep_probs(p, u.row, u.part * 256, vec_r, vec_c);
+        prep_probs(p, u.row, u.part * 256);
     if (p.x) {
         const int d8 = p.d >> 3, dp = (d8 + 127) / 128;
         uint32_t top = 0;
@@ -807,7 +813,6 @@ balance_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant
             if (!ok) break;
             // a masked row has P = 0, its sums are finite and its token_loss is not used
             const bool keep = MODE != kGrads && row < p.M && (!g.mask || g.mask[row]);
-            const bool vec = MODE == kFwd && float4_rows(p.p, p.N);
             const float l_t = MODE == kGrid && keep ? g.token_loss[row] : 0.f;
             if (MODE == kGrads) scale2 = pow2f(-top_exp(p.a_mn ? g.hdr->x_top : g.hdr->w_top));
             float part = 0.f;
@@ -820,25 +825,12 @@ balance_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant
                     // waits for another in here)
                     if (keep) {
                         const float *src = p.p + (int64_t)row * p.N + col0;
-                        if (vec && col0 + 32 <= p.N) {
 #pragma unroll
-                            for (int j = 0; j < 32; j += 16) {
-                                float4 v[4];
+                        for (int j = 0; j < 32; j += 8) {
+                            float v[8];
+                            load_logp8(src + j, p.N - col0 - j, v);
 #pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    v[k] = __ldg(reinterpret_cast<const float4 *>(src + j) + k);
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) {
-                                    part = fmaf(expf(v[k].x), sum[q][j + 4 * k], part);
-                                    part = fmaf(expf(v[k].y), sum[q][j + 4 * k + 1], part);
-                                    part = fmaf(expf(v[k].z), sum[q][j + 4 * k + 2], part);
-                                    part = fmaf(expf(v[k].w), sum[q][j + 4 * k + 3], part);
-                                }
-                            }
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                if (col0 + j < p.N) part = fmaf(expf(__ldg(src + j)), sum[q][j], part);
+                            for (int k = 0; k < 8; ++k) part = fmaf(expf(v[k]), sum[q][j + k], part);
                         }
                     }
                 } else {
