@@ -190,21 +190,29 @@ struct BalPrep {
     BalHeader *hdr;
 };
 
-// 8 log-probabilities from `at` on, of which `valid` exist (the others read as
-// -inf).  A row starts at any multiple of 4 bytes, so they come as the 2 or 3
-// aligned 16-byte chunks that hold at least one of them (what else a chunk holds
-// lies beside it in memory and is dropped), shifted into place.  At 6001 tokens
-// and 1101 x 1303 the U product takes 47 us so (58 with 4-byte loads) and the
-// preparation 50 (58); at 4096 tokens and 1304 x 1304 they take 40 and 42 us (41
-// and 42 with a branch of its own for aligned rows).
+// Whether 16-byte pieces at 16-byte boundaries that hold a value of row t of
+// p [L, N] lie within p: they reach at most 3 values past the row.
+__device__ __forceinline__ bool whole_pieces(const float *p, int64_t t, int64_t L, int N) {
+    const int beside = N >= 3 ? 1 : 3;
+    return ((reinterpret_cast<uintptr_t>(p) & 15) == 0 && (N & 3) == 0) ||
+           (t >= beside && t < L - beside);
+}
+
+// 8 log-probabilities of a row with whole_pieces, from `at` on, of which `valid`
+// exist (the others read as -inf).  A row starts at any multiple of 4 bytes, so
+// they come as the 2 or 3 pieces that hold at least one of them, shifted into
+// place; what else a piece holds is dropped.  At 6001 tokens and 1101 x 1303 the
+// U product takes 47 us so (58 with 4-byte loads) and the preparation 52 (58); at
+// 4096 tokens and 1304 x 1304 they take 40 and 42.5 us (41 and 41.5 with a branch
+// of its own for aligned rows).
 __device__ __forceinline__ void load_logp8(const float *at, int valid, float *v) {
     const int m = (int)(reinterpret_cast<uintptr_t>(at) >> 2) & 3;
-    const float4 *chunk = reinterpret_cast<const float4 *>(at - m);
+    const float4 *piece = reinterpret_cast<const float4 *>(at - m);
     float w[12];
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
         float4 c = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (4 * k - m < valid && (k < 2 || m > 0)) c = __ldg(chunk + k);
+        if (4 * k - m < valid && (k < 2 || m > 0)) c = piece[k];
         w[4 * k] = c.x, w[4 * k + 1] = c.y, w[4 * k + 2] = c.z, w[4 * k + 3] = c.w;
     }
 #pragma unroll
@@ -222,7 +230,14 @@ __device__ __forceinline__ void prep_probs(const BalPrep &p, int64_t t, int c0) 
     if (!p.mask || p.mask[t]) {
         const bool rows = c0 < p.seg_r;
         const int col = rows ? c0 : c0 - p.seg_r, n = rows ? p.N_r : p.N_c;
-        load_logp8((rows ? p.p_r + t * p.N_r : p.p_c + t * p.N_c) + col, n - col, v);
+        const float *src = rows ? p.p_r : p.p_c;
+        const float *at = src + t * n + col;
+        if (whole_pieces(src, t, p.L, n)) {
+            load_logp8(at, n - col, v);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = col + i < n ? at[i] : -INFINITY;
+        }
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = kScaleP * expf(v[i]);
     }
@@ -813,6 +828,8 @@ balance_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant
             if (!ok) break;
             // a masked row has P = 0, its sums are finite and its token_loss is not used
             const bool keep = MODE != kGrads && row < p.M && (!g.mask || g.mask[row]);
+            const bool whole = MODE == kFwd && whole_pieces(p.p, row, p.M, p.N);
+            const uint32_t apart = MODE == kFwd ? __ballot_sync(0xffffffffu, keep && !whole) : 0u;
             const float l_t = MODE == kGrid && keep ? g.token_loss[row] : 0.f;
             if (MODE == kGrads) scale2 = pow2f(-top_exp(p.a_mn ? g.hdr->x_top : g.hdr->w_top));
             float part = 0.f;
@@ -821,10 +838,15 @@ balance_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant
                 const int col0 = n0 + 32 * (half + 2 * q);
                 if (half + 2 * q >= blocks || col0 >= (MODE == kGrid ? p.seg : p.N)) break;
                 if constexpr (MODE == kFwd) {
-                    // each lane its own row: the sums stay where they are (no lane
-                    // waits for another in here)
+                    // each lane its own row: the sums stay where they are.  Rows at the
+                    // array's ends come through shared memory.
+                    for (uint32_t m = apart; m != 0; m &= m - 1) {
+                        const int r = __ffs((int)m) - 1, col = col0 + (int)lane;
+                        if (col < p.N) turn_buf[32 * r + (int)lane] = p.p[(int64_t)(row0 + r) * p.N + col];
+                    }
+                    __syncwarp();
                     if (keep) {
-                        const float *src = p.p + (int64_t)row * p.N + col0;
+                        const float *src = whole ? p.p + (int64_t)row * p.N + col0 : turn_buf + 32 * (int)lane;
 #pragma unroll
                         for (int j = 0; j < 32; j += 8) {
                             float v[8];

@@ -291,6 +291,30 @@ def test_balance_masked_rows_hold_anything():
     assert torch.equal(dx[~mask], kept[~mask])
 
 
+@pytest.mark.parametrize("L,N_r,N_c", [(1, 1, 2), (2, 3, 4), (3, 5, 66), (40, 7, 71), (37, 2, 1), (33, 40, 262)])
+@pytest.mark.parametrize("offset", [0, 1, 2, 3])
+def test_balance_axes_at_any_address(L, N_r, N_c, offset):
+    """Log-probabilities from any 4-byte boundary on, NaN around them: bit for
+    bit the results of arrays of their own."""
+    d, K = 64, 2
+    x, W_r, W_c, p_r, p_c, idx, mask = _balance_inputs(L, d, N_r, N_c, K, L, masked=True)
+    cnt = omni.expert_counts(idx, N_r * N_c, mask=mask)
+
+    def within(p):
+        room = torch.full((p.numel() + 16,), float("nan"), device=DEV)
+        at = room[4 + offset:4 + offset + p.numel()].view_as(p)
+        return at.copy_(p)
+
+    def both(p_r, p_c):
+        fwd = omni.balance_fwd(p_r, p_c, cnt["counts"], cnt["n_tokens"], K, mask=mask)
+        return {**fwd, **omni.balance_bwd(x, W_r, W_c, p_r, p_c, cnt["counts"], cnt["n_tokens"], K,
+                                          fwd["token_loss"], mask=mask)}
+
+    want, got = both(p_r, p_c), both(within(p_r), within(p_c))
+    for k in want:
+        assert torch.equal(want[k], got[k]) and torch.isfinite(got[k]).all(), k
+
+
 def test_balance_all_rows_masked():
     L, d, N_r, N_c, K = 20, 64, 8, 8, 2
     x, W_r, W_c, p_r, p_c, idx, _ = _balance_inputs(L, d, N_r, N_c, K, 2)
