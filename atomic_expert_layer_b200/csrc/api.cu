@@ -21,6 +21,11 @@ inline size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+// whether arrays of na and nb floats share memory
+bool overlap(const float *a, size_t na, const float *b, size_t nb) {
+    const uintptr_t u = reinterpret_cast<uintptr_t>(a), v = reinterpret_cast<uintptr_t>(b);
+    return u < v + sizeof(float) * nb && v < u + sizeof(float) * na;
+}
 }  // namespace
 
 int device_sm_count() {
@@ -650,6 +655,10 @@ int omni_balance_bwd(const omni_bf16 *x, const omni_bf16 *W_r, const omni_bf16 *
         return OMNI_ERR_INVALID_ARG;
     if ((rc = check_plain_ws(ws, ws_bytes, omni_balance_bwd_workspace_size(L, d, N_r, N_c))))
         return rc;
+    // a tile updates its part of a gradient with plain loads and stores
+    const size_t nx = (size_t)L * (size_t)d, nr = (size_t)N_r * (size_t)d, nc = (size_t)N_c * (size_t)d;
+    if (overlap(dx, nx, dW_r, nr) || overlap(dx, nx, dW_c, nc) || overlap(dW_r, nr, dW_c, nc))
+        return OMNI_ERR_INVALID_ARG;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if ((rc = clear_header(ws, st))) return rc;
     return cuda_rc(launch_balance_bwd(x, W_r, W_c, p_r, p_c, counts, n_tokens, mask, token_loss, L,
@@ -691,6 +700,10 @@ int omni_layer_norm_bwd(const void *x, const float *mean, const float *rstd, con
         !aligned16(dw) || !aligned16(db) || !aligned4(mean) || !aligned4(rstd))
         return OMNI_ERR_INVALID_ARG;
     if ((rc = check_plain_ws(ws, ws_bytes, omni_layer_norm_bwd_workspace_size(L, d)))) return rc;
+    const size_t nx = (size_t)L * (size_t)d, nw = (size_t)d;
+    if (overlap(dx, nx, dw, nw) || (db && (overlap(dx, nx, db, nw) || overlap(dw, nw, db, nw))) ||
+        (dx != dy && overlap(dx, nx, dy, nx)))
+        return OMNI_ERR_INVALID_ARG;
     first_launch_in_call();
     return cuda_rc(launch_norm_bwd(x, (flags & OMNI_X_F32) != 0, mean, rstd, q, scale, w, dy, L, d,
                                    dx, (flags & OMNI_DX_ACCUMULATE) != 0, dw, db,
@@ -746,6 +759,13 @@ int omni_routed_bwd_ckpt(const uint8_t *q, const uint8_t *scale, const omni_bf16
         return OMNI_ERR_INVALID_ARG;
     if ((rc = check_plain_ws(ws, ws_bytes, omni_routed_bwd_ckpt_workspace_size(L, d, N_r, N_c, K))))
         return rc;
+    const struct { const float *at; size_t n; } grads[] = {
+        {dx, (size_t)L * d}, {dW, (size_t)sz.N * d}, {dV, (size_t)sz.N * d},
+        {dW_r, (size_t)N_r * d}, {dW_c, (size_t)N_c * d}};
+    for (int i = 0; i < 5; ++i)
+        for (int j = 0; j < i; ++j)
+            if (overlap(grads[i].at, grads[i].n, grads[j].at, grads[j].n)) return OMNI_ERR_INVALID_ARG;
+    if (overlap(dx, grads[0].n, dy, grads[0].n)) return OMNI_ERR_INVALID_ARG;
     const size_t bwd = omni_routed_bwd_workspace_size(L, d, N_r, N_c, K);
     uint16_t *x = ws_at<uint16_t>(ws, bwd);
     if ((rc = omni_act_unpack(q, scale, w, b, L, d, x, stream))) return rc;

@@ -372,8 +372,8 @@ int omni_expert_counts(const int32_t *idx, const uint8_t *mask, int L, int K, in
  * finite one, to 2^-39 of it below).  Every output element is written by one tile: the results are
  * the same on every run.
  * ws: the size functions' bytes, 256-byte aligned.  dx, dW_r, dW_c, x, W_r,
- * W_c 16-byte aligned.  d % 8 == 0.  Limits: N_r, N_c <= OMNI_MAX_AXIS,
- * L <= 2^30.
+ * W_c 16-byte aligned; dx, dW_r and dW_c share no memory (OMNI_ERR_INVALID_ARG).
+ * d % 8 == 0.  Limits: N_r, N_c <= OMNI_MAX_AXIS, L <= 2^30.
  */
 size_t omni_balance_fwd_workspace_size(int L, int N_r, int N_c);
 int omni_balance_fwd(const float *p_r, const float *p_c, const int32_t *counts,
@@ -411,7 +411,7 @@ int omni_layer_norm_fwd(const void *x, const omni_bf16 *w, const omni_bf16 *b, i
  *   dx [L, d] fp32 output, or added to dx with OMNI_DX_ACCUMULATE; dx may be dy
  *   (without the flag)
  *   dw [d], db [d] fp32  accumulated (+=; = with OMNI_DW_OVERWRITE): sum_t dy xh,
- *   sum_t dy; db may be NULL
+ *   sum_t dy; db may be NULL; dx, dw and db share no memory
  * The sums over the rows run in a fixed order: the results are the same on
  * every run.  ws: omni_layer_norm_bwd_workspace_size(L, d) bytes, 256-byte
  * aligned.  Limits as for the forward; fp32 arrays 16-byte aligned (mean,
@@ -448,7 +448,8 @@ int omni_act_unpack(const uint8_t *q, const uint8_t *scale, const omni_bf16 *w,
  * x = omni_act_unpack(q, scale, w, b), then the same arguments and results
  * (dx is the gradient with respect to that x).  The experts and the router
  * see the restored tokens; idx and gate are the forward's.  With
- * OMNI_DW_OVERWRITE the call clears dW, dV, dW_r and dW_c first.
+ * OMNI_DW_OVERWRITE the call clears dW, dV, dW_r and dW_c first.  The
+ * gradients and dy share no memory (OMNI_ERR_INVALID_ARG).
  * ws: omni_routed_bwd_ckpt_workspace_size(...) bytes, 256-byte aligned (the
  * fast path's workspace and the restored tokens, 2 L d bytes).
  */

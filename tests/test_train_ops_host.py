@@ -25,6 +25,7 @@ def _p(v):
 FAKE = _p(1 << 20)                       # 16-byte aligned, never dereferenced
 ODD = _p((1 << 20) + 2)
 BIG = 1 << 34
+APART = [_p(i << 24) for i in range(2, 7)]       # five gradients that share no memory
 
 
 # ------------------------------------------------------------- references
@@ -146,7 +147,7 @@ def test_balance_refusals(lib):
         bad = list(ok)
         bad[at] = v
         assert lib.omni_balance_fwd(*bad) == rc, (at, v)
-    ok = [FAKE] * 7 + [None, FAKE, 4, 64, 8, 8, 2, 1.0, FAKE, FAKE, FAKE, 0, FAKE, BIG, None]
+    ok = [FAKE] * 7 + [None, FAKE, 4, 64, 8, 8, 2, 1.0, *APART[:3], 0, FAKE, BIG, None]
     _try_all_pointers(lib.omni_balance_bwd, ok, (0, 1, 2, 3, 4, 5, 6, 8, 15, 16, 17, 19))
     for at, v, rc in ((9, 0, -1), (10, 0, -1), (10, 12, -2), (11, 9000, -2), (13, 0, -1), (18, 1, -1),
                       (20, 1000, -3), (0, ODD, -1), (15, _p((1 << 20) + 4), -1), (3, ODD, -1), (9, (1 << 30) + 1, -2)):
@@ -167,7 +168,7 @@ def test_layer_norm_refusals(lib):
     # a checkpoint needs whole blocks of 32
     assert lib.omni_layer_norm_fwd(FAKE, FAKE, None, 4, 40, 1e-5, FAKE, None, None, FAKE, FAKE, 0,
                                    None) == -2
-    ok = [FAKE, FAKE, FAKE, None, None, FAKE, FAKE, 4, 64, FAKE, FAKE, None, 0, FAKE, BIG, None]
+    ok = [FAKE, FAKE, FAKE, None, None, FAKE, FAKE, 4, 64, APART[0], APART[1], None, 0, FAKE, BIG, None]
     _try_all_pointers(lib.omni_layer_norm_bwd, ok, (0, 1, 2, 5, 6, 9, 10, 13))
     for at, v, rc in ((7, 0, -1), (8, 12, -2), (3, FAKE, -1), (4, FAKE, -1), (12, 2, -1), (14, 100, -3),
                       (6, ODD, -1), (13, _p((1 << 20) + 8), -1), (11, ODD, -1)):
@@ -189,13 +190,41 @@ def test_checkpoint_refusals(lib):
         bad = list(ok)
         bad[at] = v
         assert lib.omni_act_unpack(*bad) == rc, (at, v)
-    ok = [FAKE, FAKE, None, None, FAKE, FAKE, FAKE, FAKE, 4, 256, 8, 8, 2] + [FAKE] * 8 + [0, FAKE, BIG, None]
+    ok = [FAKE, FAKE, None, None, FAKE, FAKE, FAKE, FAKE, 4, 256, 8, 8, 2] + [FAKE] * 3 + APART + [0, FAKE, BIG, None]
     _try_all_pointers(lib.omni_routed_bwd_ckpt, ok, (0, 1, 4, 5, 6, 7, *range(13, 21), 22))
     for at, v, rc in ((8, 0, -1), (9, 264, -2), (12, 65, -1), (21, 1, -1), (23, 256, -3), (3, FAKE, -1),
                       (16, ODD, -1)):
         bad = list(ok)
         bad[at] = v
         assert lib.omni_routed_bwd_ckpt(*bad) == rc, (at, v)
+
+
+@pytest.mark.parametrize("shift", [0, 1, 2])
+def test_gradients_that_share_memory_are_refused(lib, shift):
+    """One buffer for two gradients, or one that begins inside another: their
+    tiles would update it at the same time."""
+    def refused(fn, args, at, n):
+        for i, a in enumerate(at):
+            for b in at[:i]:
+                bad = list(args)
+                bad[b] = _p(args[a].value - (0, 16, -4 * (n[i] - 4))[shift])
+                assert fn(*bad) == -1, (a, b)
+
+    L, d, N_r, N_c = 4, 256, 12, 8
+    tied = [FAKE] * 7 + [None, FAKE, L, d, N_r, N_c, 2, 1.0, *APART[:3], 0, FAKE, BIG, None]
+    refused(lib.omni_balance_bwd, tied, (15, 16, 17), (L * d, N_r * d, N_c * d))
+    norm = [FAKE, FAKE, FAKE, None, None, FAKE, _p(9 << 24), L, d, *APART[:3], 0, FAKE, BIG, None]
+    refused(lib.omni_layer_norm_bwd, norm, (9, 10, 11), (L * d, d, d))
+    if shift:
+        # dx may be dy, but not begin inside it
+        norm[9] = _p(norm[6].value + 16 * (2 * shift - 3))
+        assert lib.omni_layer_norm_bwd(*norm) == -1
+    routed = [FAKE, FAKE, None, None, FAKE, FAKE, FAKE, FAKE, L, d, N_r, N_c, 2, FAKE, FAKE, FAKE,
+              *APART, 0, FAKE, BIG, None]
+    refused(lib.omni_routed_bwd_ckpt, routed, (16, 17, 18, 19, 20),
+            (L * d, N_r * N_c * d, N_r * N_c * d, N_r * d, N_c * d))
+    routed[15] = _p(APART[0].value + 16 * shift)                 # nor dx and dy
+    assert lib.omni_routed_bwd_ckpt(*routed) == -1
 
 
 def test_wrappers_refuse_cpu_tensors(lib):
