@@ -391,7 +391,7 @@ def layer_norm_bwd(dy, w, rstd, x=None, mean=None, q=None, scale=None, bias=True
                    db=None, ws=None, stream=None):
     """Backward of layer_norm_fwd from its kept input (x, mean) or from its
     checkpoint (q, scale).  With a given dx the gradient is added to it (the
-    residual's), else a new one is returned; dw and (with bias) db are
+    residual's; it may be dy), else a new one is returned; dw and (with bias) db are
     accumulated into the given fp32 buffers (new ones if None)."""
     L, d, di = _rows("dy", dy)
     if (q is not None and x is not None) or (db is not None and not bias):

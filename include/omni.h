@@ -409,7 +409,8 @@ int omni_layer_norm_fwd(const void *x, const omni_bf16 *w, const omni_bf16 *b, i
  *   g = dy w,  dx = rstd (g - mean(g) - xh mean(g xh))
  *   dy [L, d] fp32 (omni_routed_bwd's dx);  rstd [L] fp32 of the forward
  *   dx [L, d] fp32 output, or added to dx with OMNI_DX_ACCUMULATE; dx may be dy
- *   (without the flag)
+ *   (with the flag: dy plus the gradient, what a residual around the norm alone
+ *   passes on)
  *   dw [d], db [d] fp32  accumulated (+=; = with OMNI_DW_OVERWRITE): sum_t dy xh,
  *   sum_t dy; db may be NULL; dx, dw and db share no memory
  * The sums over the rows run in a fixed order: the results are the same on

@@ -504,6 +504,11 @@ def test_layer_norm_gradients_accumulate_and_repeat():
     omni.omni_layer_norm_bwd(x, f["mean"], f["rstd"], None, None, w, inplace, L, d, inplace, dw, db,
                              omni.OMNI_X_F32, ws)
     assert torch.equal(inplace, one["dx"]) and torch.equal(dw, one["dw"]) and torch.equal(db, one["db"])
+    # dx added to dy itself
+    inplace = dy.clone()
+    got = omni.layer_norm_bwd(inplace, w, f["rstd"], **kept, dx=inplace)
+    assert torch.equal(inplace, dy + one["dx"])
+    assert torch.equal(got["dw"], one["dw"]) and torch.equal(got["db"], one["db"])
 
 
 def test_overwrite_does_not_read_the_gradients():
