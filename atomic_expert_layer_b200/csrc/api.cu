@@ -762,10 +762,11 @@ int omni_routed_bwd_ckpt(const uint8_t *q, const uint8_t *scale, const omni_bf16
     const struct { const float *at; size_t n; } grads[] = {
         {dx, (size_t)L * d}, {dW, (size_t)sz.N * d}, {dV, (size_t)sz.N * d},
         {dW_r, (size_t)N_r * d}, {dW_c, (size_t)N_c * d}};
-    for (int i = 0; i < 5; ++i)
+    for (int i = 0; i < 5; ++i) {
+        if (overlap(grads[i].at, grads[i].n, dy, grads[0].n)) return OMNI_ERR_INVALID_ARG;
         for (int j = 0; j < i; ++j)
             if (overlap(grads[i].at, grads[i].n, grads[j].at, grads[j].n)) return OMNI_ERR_INVALID_ARG;
-    if (overlap(dx, grads[0].n, dy, grads[0].n)) return OMNI_ERR_INVALID_ARG;
+    }
     const size_t bwd = omni_routed_bwd_workspace_size(L, d, N_r, N_c, K);
     uint16_t *x = ws_at<uint16_t>(ws, bwd);
     if ((rc = omni_act_unpack(q, scale, w, b, L, d, x, stream))) return rc;

@@ -227,6 +227,21 @@ def test_gradients_that_share_memory_are_refused(lib, shift):
     assert lib.omni_routed_bwd_ckpt(*routed) == -1
 
 
+@pytest.mark.parametrize("at", range(5), ids=["dx", "dW", "dV", "dW_r", "dW_c"])
+@pytest.mark.parametrize("shift", [0, 16, -1])
+def test_no_gradient_shares_memory_with_dy(lib, at, shift):
+    """Clearing or adding to a gradient would change the dy that the backward
+    reads: every one of the five at dy, inside it, and reaching into it."""
+    L, d, N_r, N_c = 4, 256, 12, 8
+    n = (L * d, N_r * N_c * d, N_r * N_c * d, N_r * d, N_c * d)
+    args = [FAKE, FAKE, None, None, FAKE, FAKE, FAKE, FAKE, L, d, N_r, N_c, 2, FAKE, FAKE, _p(9 << 24),
+            *APART, 0, FAKE, BIG, None]
+    args[16 + at] = _p((9 << 24) + (shift if shift >= 0 else 16 - 4 * n[at]))
+    for flags in (0, omni.OMNI_DW_OVERWRITE):
+        args[21] = flags
+        assert lib.omni_routed_bwd_ckpt(*args) == -1
+
+
 def test_wrappers_refuse_cpu_tensors(lib):
     x = torch.zeros(4, 64, dtype=torch.bfloat16)
     w = torch.zeros(64, dtype=torch.bfloat16)
