@@ -533,7 +533,7 @@ int omni_routed_bwd(const omni_bf16 *x, const omni_bf16 *W, const omni_bf16 *V,
     if (d % 256 != 0 || d > OMNI_MAX_D) return OMNI_ERR_UNSUPPORTED;
     if (!aligned16(x) || !aligned16(W) || !aligned16(V) || !aligned16(W_r) || !aligned16(W_c) ||
         !aligned16(dy) || !aligned16(dx) || !aligned16(dW) || !aligned16(dV) ||
-        !aligned16(dW_r) || !aligned16(dW_c))
+        !aligned16(dW_r) || !aligned16(dW_c) || !aligned4(idx) || !aligned4(gate))
         return OMNI_ERR_INVALID_ARG;
     if (ws_bytes < sizeof(WsHeader) || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
         return OMNI_ERR_WORKSPACE;
@@ -755,7 +755,8 @@ int omni_routed_bwd_ckpt(const uint8_t *q, const uint8_t *scale, const omni_bf16
         return OMNI_ERR_INVALID_ARG;
     if (d % 256 != 0 || d > OMNI_MAX_D) return OMNI_ERR_UNSUPPORTED;
     if (!aligned16(W) || !aligned16(V) || !aligned16(W_r) || !aligned16(W_c) || !aligned16(dy) ||
-        !aligned16(dx) || !aligned16(dW) || !aligned16(dV) || !aligned16(dW_r) || !aligned16(dW_c))
+        !aligned16(dx) || !aligned16(dW) || !aligned16(dV) || !aligned16(dW_r) || !aligned16(dW_c) ||
+        !aligned4(idx) || !aligned4(gate))
         return OMNI_ERR_INVALID_ARG;
     if ((rc = check_plain_ws(ws, ws_bytes, omni_routed_bwd_ckpt_workspace_size(L, d, N_r, N_c, K))))
         return rc;

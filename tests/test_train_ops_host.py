@@ -242,6 +242,19 @@ def test_no_gradient_shares_memory_with_dy(lib, at, shift):
         assert lib.omni_routed_bwd_ckpt(*args) == -1
 
 
+@pytest.mark.parametrize("at", [0, 1], ids=["idx", "gate"])
+def test_routed_bwd_refuses_misaligned_routing(lib, at):
+    """idx and gate are read 4 bytes at a time: off that grid they are refused
+    on the host, as the other arrays are."""
+    ckpt = [FAKE, FAKE, None, None, FAKE, FAKE, FAKE, FAKE, 4, 256, 8, 8, 2, FAKE, FAKE, _p(9 << 24),
+            *APART, 0, FAKE, BIG, None]
+    ckpt[13 + at] = ODD
+    assert lib.omni_routed_bwd_ckpt(*ckpt) == -1
+    bwd = [FAKE] * 5 + [4, 256, 8, 8, 2, FAKE, FAKE, _p(9 << 24), *APART, 0, FAKE, BIG, None]
+    bwd[10 + at] = ODD
+    assert lib.omni_routed_bwd(*bwd) == -1
+
+
 def test_wrappers_refuse_cpu_tensors(lib):
     x = torch.zeros(4, 64, dtype=torch.bfloat16)
     w = torch.zeros(64, dtype=torch.bfloat16)
