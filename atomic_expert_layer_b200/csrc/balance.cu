@@ -83,13 +83,24 @@ struct BalHeader {
     uint32_t x_top;      // largest finite magnitude of the kept rows of x, as bits
     uint32_t w_top;      // ... of W_r and W_c
 };
-// Exponent that takes a magnitude below 2^15 (its bits as fp32, subnormals
-// and numbers below 2^-60 as 2^-60), and the two powers of two.
+// Exponent that takes a magnitude below 2^15 (its bits as fp32, subnormals as
+// 2^-126): up to 140.
 __device__ __forceinline__ int top_exp(uint32_t bits) {
     const int e = (int)(bits >> 23) - 127;
-    return 14 - (e < -60 ? -60 : e);
+    return 14 - (e < -126 ? -126 : e);
 }
 __device__ __forceinline__ float pow2f(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+// 2^e as two factors, since fp32 holds powers from 2^-126 to 2^127 only.
+// Between them a product is never above both its value and its result, and
+// below fp32's normal range only where the result is too.
+struct Pow2 {
+    float a, b;
+    __device__ explicit Pow2(int e) {
+        e = e < -252 ? -252 : e > 252 ? 252 : e;
+        a = pow2f(e >> 1);
+        b = pow2f(e - (e >> 1));
+    }
+};
 // P (U - l) / 2^count_exp is below 1
 __device__ __forceinline__ int count_exp(int most) { return 32 - __clz(most); }
 
@@ -404,7 +415,7 @@ struct BalCast {
 __global__ void __launch_bounds__(kPrepThreads) balance_cast_kernel(const BalCast p) {
     grid_dependency_wait();
     grid_dependents_launch();
-    const float sx = pow2f(top_exp(p.hdr->x_top)), sw = pow2f(top_exp(p.hdr->w_top));
+    const Pow2 sx(top_exp(p.hdr->x_top)), sw(top_exp(p.hdr->w_top));
     const int d8 = p.d >> 3;
     const int64_t warps = (int64_t)gridDim.x * (kPrepThreads / 32);
     for (int64_t row = (int64_t)blockIdx.x * (kPrepThreads / 32) + (threadIdx.x >> 5);
@@ -420,7 +431,7 @@ __global__ void __launch_bounds__(kPrepThreads) balance_cast_kernel(const BalCas
             src = p.W_c + (r - p.pr) * p.d;
         }
         uint4 *dst = reinterpret_cast<uint4 *>((w ? p.w16 : p.x16) + r * p.d);
-        const float s = w ? sw : sx;
+        const Pow2 s = w ? sw : sx;
         for (int c = (int)lane_id(); c < d8; c += 32) {
             uint4 o = make_uint4(0, 0, 0, 0);
             if (src) {
@@ -429,8 +440,8 @@ __global__ void __launch_bounds__(kPrepThreads) balance_cast_kernel(const BalCas
                 uint32_t h[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const __half2 b = __floats2half2_rn(__uint_as_float(a[i] << 16) * s,
-                                                        __uint_as_float(a[i] & 0xffff0000u) * s);
+                    const __half2 b = __floats2half2_rn(__uint_as_float(a[i] << 16) * s.a * s.b,
+                                                        __uint_as_float(a[i] & 0xffff0000u) * s.a * s.b);
                     h[i] = *reinterpret_cast<const uint32_t *>(&b);
                 }
                 o = make_uint4(h[0], h[1], h[2], h[3]);
@@ -523,7 +534,7 @@ struct GemmArgs {
     float *part;                  // forward: sums over a tile's columns [tiles_n * 2, L]
     const float *token_loss;      // backward
     const int32_t *n_tokens;
-    float factor;                 // dloss N / K
+    double factor;                // dloss N / K
     BalHeader *hdr;
 };
 struct GemmMaps { CUtensorMap m[kMaxMaps]; };
@@ -753,14 +764,18 @@ balance_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant
         const int half = (warp - 2) >> 2;
         const uint32_t tempty = smem_in_cta(&sm.tempty[0], 0);
         float *turn_buf = sm.turn[warp - 2];
-        // kGrid: ds / c to below 2^15, and P's 2^14 out; kGrads: that scale out,
-        // the operand's (scale2), and c in
-        float scale1 = 1.f, scale2 = 1.f, coef = 0.f;
+        // kGrid: ds / c to below 2^15, and P's 2^14 out; kGrads: c in, as a
+        // number of magnitude 1 to 2 and an exponent that the scales join
+        float scale1 = 1.f, coef = 0.f;
+        int coef_exp = 0;
         if (MODE == kGrid) scale1 = pow2f(1 - count_exp(g.hdr->most));
         if (MODE == kGrads) {
             const int n = *g.n_tokens, kept = g.hdr->kept;
-            if (n > 0 && kept > 0) coef = g.factor / (float)n / (float)kept;
-            scale1 = pow2f(count_exp(g.hdr->most) - 15);
+            if (n > 0 && kept > 0) {
+                const double c = g.factor / n / kept;
+                if (c != 0.0 && isfinite(c)) coef_exp = ilogb(c);
+                coef = (float)scalbn(c, -coef_exp);
+            }
         }
         int buf = 0, wrap = 0;
         bool ok = true;
@@ -831,7 +846,10 @@ balance_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant
             const bool whole = MODE == kFwd && whole_pieces(p.p, row, p.M, p.N);
             const uint32_t apart = MODE == kFwd ? __ballot_sync(0xffffffffu, keep && !whole) : 0u;
             const float l_t = MODE == kGrid && keep ? g.token_loss[row] : 0.f;
-            if (MODE == kGrads) scale2 = pow2f(-top_exp(p.a_mn ? g.hdr->x_top : g.hdr->w_top));
+            // kGrads: the scales of ds and of the other operand, out again
+            const Pow2 out_scale(MODE == kGrads ? coef_exp + count_exp(g.hdr->most) - 15 -
+                                                      top_exp(p.a_mn ? g.hdr->x_top : g.hdr->w_top)
+                                                : 0);
             float part = 0.f;
 #pragma unroll
             for (int q = 0; q < kEpiBlocks; ++q) {
@@ -857,7 +875,9 @@ balance_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant
                     }
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) turn_buf[turned((int)lane, j)] = sum[q][j];
+                    for (int j = 0; j < 32; ++j)
+                        turn_buf[turned((int)lane, j)] =
+                            MODE == kGrads ? sum[q][j] * coef * out_scale.a * out_scale.b : sum[q][j];
                     __syncwarp();
                 }
                 if constexpr (MODE == kGrid) {
@@ -923,10 +943,10 @@ balance_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant
                         for (int i = 0; i < 4; ++i) {
                             const int r = r0 + 4 * (i4 + i);
                             float4 v;
-                            v.x = __fmul_rn(turn_buf[turned(r, c)] * scale1 * scale2, coef);
-                            v.y = __fmul_rn(turn_buf[turned(r, c + 1)] * scale1 * scale2, coef);
-                            v.z = __fmul_rn(turn_buf[turned(r, c + 2)] * scale1 * scale2, coef);
-                            v.w = __fmul_rn(turn_buf[turned(r, c + 3)] * scale1 * scale2, coef);
+                            v.x = turn_buf[turned(r, c)];
+                            v.y = turn_buf[turned(r, c + 1)];
+                            v.z = turn_buf[turned(r, c + 2)];
+                            v.w = turn_buf[turned(r, c + 3)];
                             if (p.accumulate) {
                                 v.x += prev[i].x;
                                 v.y += prev[i].y;
@@ -1241,7 +1261,7 @@ cudaError_t launch_balance_bwd(const uint16_t *x, const uint16_t *W_r, const uin
 
     GemmArgs h = {};
     h.hdr = pp.hdr; h.n_tokens = n_tokens;
-    h.factor = (float)((double)dloss * N_r * N_c / K);
+    h.factor = (double)dloss * N_r * N_c / K;
     h.nprob = 2;
     const int nk_dw = (L + BK - 1) / BK, nk_dx = w.ld / BK;
     GemmProb &dw = h.prob[nk_dw < nk_dx];            // A is ds^T, K the tokens

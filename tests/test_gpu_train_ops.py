@@ -355,6 +355,67 @@ def test_balance_counts_summed_over_replicas():
         _within(got[name], want[name], (delta + 2.0 ** -15) * want[name + "_abs"] + 1e-30, name)
 
 
+# Bars that hold the balance gradients to fp32's accuracy, relative to the
+# results however small they are.  Rounding errors of single terms average out
+# of a norm; what stays is the tensor core's cutting off towards zero, 2^-24 of
+# the running sum at an instruction on average.  Over the 16 to 32 instructions
+# of an accumulator, whose sum grows as they go, that is 3e-7 to 6e-7 of a
+# product, and 2e-6 with four times as many: 1.5e-6 is asked for.  Where U and
+# l cancel, the errors of U and of l (2^-24 of themselves at a rounding each,
+# two of them) do not shrink with their difference: l's shifts a token's whole
+# row by 2^-23 c P l, U's are one by one (root of the sum of squares).
+BAR = 1.5e-6
+
+
+def _cancelled(x, W_r, W_c, p_r, p_c, counts, n, K, dloss, mask):
+    """Norms behind dx, dW_r and dW_c where U and l cancel: of the shift by c P l
+    in each, and of the separate terms c P (U + l)."""
+    keep = torch.ones(len(x), dtype=torch.bool, device=DEV) if mask is None else mask.bool()
+    Pr, Pc = (p[keep].double().exp() for p in (p_r, p_c))
+    F = counts.double().reshape(Pr.shape[1], Pc.shape[1])
+    U, V = Pc @ F.T, Pr @ F
+    tl = (Pr * U).sum(1, keepdim=True)
+    c = abs(dloss) * F.numel() / (K * n * int(keep.sum()))
+    xd, wr, wc = x[keep].double(), W_r.double(), W_c.double()
+    shift = dict(dx=c * tl * (Pr @ wr + Pc @ wc), dW_r=c * (Pr * tl).T @ xd, dW_c=c * (Pc * tl).T @ xd)
+    Ar, Ac = (c * Pr * (U + tl)).square(), (c * Pc * (V + tl)).square()
+    each = dict(dx=Ar @ wr.square() + Ac @ wc.square(), dW_r=Ar.T @ xd.square(), dW_c=Ac.T @ xd.square())
+    return {k: float(shift[k].norm() + each[k].sum().sqrt()) for k in shift}
+
+
+def _check_balance_to_fp32(x, W_r, W_c, p_r, p_c, counts, n_tokens, K, dloss=1.0, mask=None, cancels=True):
+    """Gradients within BAR of their norm (with `cancels` also 2^-23 of what
+    cancels), every token's loss within 2^-18 of itself.  That is the sum of: 2^-20
+    cut off in 16 instructions at worst, over a growing sum; 2^-20 for the up to
+    150 additions after them (5 times the root of the sum of squares of 2^-24 each
+    uniformly); 2^-21 for exp and the halves of P, and 2^-22 for the other exp."""
+    n = n_tokens.item()
+    want = ref.balance_ref(x, W_r, W_c, p_r, p_c, counts, n, K, dloss, mask)
+    fwd = omni.balance_fwd(p_r, p_c, counts, n_tokens, K, mask=mask)
+    floor = 2.0 ** -36 * float(counts.max())             # P's 2^-39 of 1, beside the largest count
+    _within(fwd["token_loss"], want["token_loss"], 2.0 ** -18 * want["token_loss"] + floor, "token_loss")
+    _within(fwd["loss"], want["loss"], 2.0 ** -18 * want["loss"], "loss")
+    got = omni.balance_bwd(x, W_r, W_c, p_r, p_c, counts, n_tokens, K, fwd["token_loss"], dloss=dloss, mask=mask)
+    more = _cancelled(x, W_r, W_c, p_r, p_c, counts, n, K, dloss, mask) if cancels else {}
+    for k in ("dx", "dW_r", "dW_c"):
+        err, norm = float((got[k].double() - want[k]).norm()), float(want[k].norm())
+        assert norm > 0 and err <= BAR * norm + 2.0 ** -23 * more.get(k, 0.0), (k, err / norm)
+    return fwd, got, want
+
+
+@pytest.mark.parametrize("ex,ew,dloss", [(0, -101, 1.0), (-101, 0, 1.0), (-118, -118, 2.0 ** 40),
+                                         (-128, -129, 2.0 ** 50), (120, -20, 2.0 ** -30), (-60, 122, 2.0 ** -30),
+                                         (0, 0, 2.0 ** -100), (100, 100, 2.0 ** -140)])
+def test_balance_operands_of_any_magnitude(ex, ew, dloss):
+    """x and W from bf16's subnormal numbers to near its largest, weights of the
+    loss to match: as near to their gradients as ordinary ones."""
+    x, W_r, W_c, p_r, p_c, idx, _ = _balance_inputs(150, 64, 40, 70, 5, 3)
+    x, W_r, W_c = (t.float() * 2.0 ** (e // 2) * 2.0 ** (e - e // 2) for t, e in ((x, ex), (W_r, ew), (W_c, ew)))
+    x, W_r, W_c = (t.to(torch.bfloat16) for t in (x, W_r, W_c))
+    cnt = omni.expert_counts(idx, 40 * 70)
+    _check_balance_to_fp32(x, W_r, W_c, p_r, p_c, cnt["counts"], cnt["n_tokens"], 5, dloss=dloss)
+
+
 # ------------------------------------------------------------------ norm
 def _rows(L, d, dtype, seed):
     g = _gen(seed)
