@@ -25,10 +25,12 @@
 //   P by 2^14 (22 bits, or 2^-39 of 1 where that is coarser);
 //   counts by 2^-16: exact up to 2048.  When some count is larger, what its
 //     rounding leaves is a second matrix F_lo, and hi * F_lo is added;
-//   ds / c = P (U - l_t), whose magnitude no more than the largest count
-//     bounds, so that this bound becomes 2^15;
-//   x and W, bf16: so that their largest finite magnitude becomes 2^14 to
-//     2^15.  fp16 then holds every bf16 value down to 2^-32 of it exactly.
+//   ds / c = P (U - l): a token's by the power of two that takes its l, which
+//     bounds them, to 2^13 to 2^14.  dx gets it out again row by row; for dW,
+//     which sums over tokens, the token's row of x carries it;
+//   x (with the token's power) and W, bf16: so that their largest finite
+//     magnitude becomes 2^14 to 2^15.  fp16 then holds every bf16 value down to
+//     2^-32 of it exactly.
 // bf16 halves (16 bits) need no scales, but left dx and dW off by 2.9e-6 of
 // themselves, and by 4e-3 for a collapsed router, where U - l_t cancels.  With
 // these, and with what kChunk below says, the results are as near to 64 bits
@@ -80,14 +82,24 @@ struct BalHeader {
     int most;            // largest count
     int kept;            // tokens of this batch with mask != 0
     int done;            // CTAs that have finished (forward)
-    uint32_t x_top;      // largest finite magnitude of the kept rows of x, as bits
-    uint32_t w_top;      // ... of W_r and W_c
+    int x_top;           // largest exponent of the kept rows of x, each with its token's
+                         // (kNoExp more; 0: no value but zeros)
+    int w_top;           // ... of W_r and W_c
 };
-// Exponent that takes a magnitude below 2^15 (its bits as fp32, subnormals as
-// 2^-126): up to 140.
-__device__ __forceinline__ int top_exp(uint32_t bits) {
+constexpr int kNoExp = 512;
+// Exponent of a finite magnitude, from its bits as fp32 (subnormals as 2^-126).
+__device__ __forceinline__ int exp_of(uint32_t bits) {
     const int e = (int)(bits >> 23) - 127;
-    return 14 - (e < -126 ? -126 : e);
+    return e < -126 ? -126 : e;
+}
+// Exponent by which a token's ds is scaled, from its loss: P U and P l are at
+// most l, since all terms of l = sum P U are positive and P <= 1, so no |P (U - l)|
+// is above it, and the largest is near it where the token's losses lie on few
+// experts.  Below 2^-60 some P is under 2^-30 and has lost its last bits already;
+// above 2^40 is no finite l of counts below 2^31.
+__device__ __forceinline__ int token_exp(float l) {
+    const int e = exp_of(__float_as_uint(l) & 0x7fffffffu);
+    return e < -60 ? -60 : e > 40 ? 40 : e;
 }
 __device__ __forceinline__ float pow2f(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 // 2^e as two factors, since fp32 holds powers from 2^-126 to 2^127 only.
@@ -101,8 +113,6 @@ struct Pow2 {
         b = pow2f(e - (e >> 1));
     }
 };
-// P (U - l) / 2^count_exp is below 1
-__device__ __forceinline__ int count_exp(int most) { return 32 - __clz(most); }
 
 // ----------------------------------------------------------------- counts
 __global__ void counts_clear_kernel(int32_t *__restrict__ counts, int64_t N,
@@ -194,6 +204,7 @@ struct BalPrep {
     const int32_t *counts;
     const uint8_t *mask;
     const uint16_t *x, *W_r, *W_c;   // backward (else null): their largest magnitudes are wanted
+    const float *token_loss;      // ..., beside x's
     int L, N_r, N_c, d;
     int seg_r, ld;                // columns of the row segment, and of P (0: only the column axis)
     int pc, pr;                   // padded N_c, N_r
@@ -379,15 +390,18 @@ __global__ void __launch_bounds__(kPrepThreads, kPrepPerSm) balance_prep_kernel(
         prep_probs(p, u.row, u.part * 256);
     if (p.x) {
         const int d8 = p.d >> 3, dp = (d8 + 127) / 128;
-        uint32_t top = 0;
-        for (Pieces u(w0, warps, dp); u.row < p.L; u.next())
-            if (!p.mask || p.mask[u.row]) top = max(top, top_row(p.x + u.row * p.d, u.part, d8));
+        int top = 0;
+        for (Pieces u(w0, warps, dp); u.row < p.L; u.next()) {
+            if (p.mask && !p.mask[u.row]) continue;
+            const uint32_t m = top_row(p.x + u.row * p.d, u.part, d8);
+            if (m) top = max(top, kNoExp + exp_of(m) + token_exp(p.token_loss[u.row]));
+        }
         cta_max(top, &p.hdr->x_top);
-        top = 0;
+        uint32_t w_top = 0;
         for (Pieces u(w0, warps, dp); u.row < p.N_r + p.N_c; u.next())
-            top = max(top, top_row(u.row < p.N_r ? p.W_r + u.row * p.d
-                                                 : p.W_c + (u.row - p.N_r) * p.d, u.part, d8));
-        cta_max(top, &p.hdr->w_top);
+            w_top = max(w_top, top_row(u.row < p.N_r ? p.W_r + u.row * p.d
+                                                     : p.W_c + (u.row - p.N_r) * p.d, u.part, d8));
+        cta_max(w_top ? kNoExp + exp_of(w_top) : 0, &p.hdr->w_top);
     }
     if (!p.mask) {
         if (blockIdx.x == 0 && threadIdx.x == 0) p.hdr->kept = p.L;
@@ -402,12 +416,14 @@ __global__ void __launch_bounds__(kPrepThreads, kPrepPerSm) balance_prep_kernel(
     }
 }
 
-// x and W in fp16, scaled: masked rows of x as zeros (what they hold must not
-// meet a zero gradient as NaN), W_r and W_c one under the other with zero rows
-// between, as the columns of ds lie.
+// x and W in fp16, scaled: each row of x also by its token's power of two, which
+// its ds lacks; masked rows of x as zeros (what they hold must not meet a zero
+// gradient as NaN), W_r and W_c one under the other with zero rows between, as
+// the columns of ds lie.
 struct BalCast {
     const uint16_t *x, *W_r, *W_c;
     const uint8_t *mask;
+    const float *token_loss;
     int L, N_r, N_c, d, pr, ld;
     uint16_t *x16, *w16;
     const BalHeader *hdr;
@@ -415,7 +431,7 @@ struct BalCast {
 __global__ void __launch_bounds__(kPrepThreads) balance_cast_kernel(const BalCast p) {
     grid_dependency_wait();
     grid_dependents_launch();
-    const Pow2 sx(top_exp(p.hdr->x_top)), sw(top_exp(p.hdr->w_top));
+    const int x_exp = 14 + kNoExp - p.hdr->x_top, w_exp = 14 + kNoExp - p.hdr->w_top;
     const int d8 = p.d >> 3;
     const int64_t warps = (int64_t)gridDim.x * (kPrepThreads / 32);
     for (int64_t row = (int64_t)blockIdx.x * (kPrepThreads / 32) + (threadIdx.x >> 5);
@@ -431,7 +447,7 @@ __global__ void __launch_bounds__(kPrepThreads) balance_cast_kernel(const BalCas
             src = p.W_c + (r - p.pr) * p.d;
         }
         uint4 *dst = reinterpret_cast<uint4 *>((w ? p.w16 : p.x16) + r * p.d);
-        const Pow2 s = w ? sw : sx;
+        const Pow2 s(w ? w_exp : x_exp + (src ? token_exp(p.token_loss[r]) : 0));
         for (int c = (int)lane_id(); c < d8; c += 32) {
             uint4 o = make_uint4(0, 0, 0, 0);
             if (src) {
@@ -764,11 +780,9 @@ balance_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant
         const int half = (warp - 2) >> 2;
         const uint32_t tempty = smem_in_cta(&sm.tempty[0], 0);
         float *turn_buf = sm.turn[warp - 2];
-        // kGrid: ds / c to below 2^15, and P's 2^14 out; kGrads: c in, as a
-        // number of magnitude 1 to 2 and an exponent that the scales join
-        float scale1 = 1.f, coef = 0.f;
+        // kGrads: c, as a number of magnitude 1 to 2 and an exponent that the scales join
+        float coef = 0.f;
         int coef_exp = 0;
-        if (MODE == kGrid) scale1 = pow2f(1 - count_exp(g.hdr->most));
         if (MODE == kGrads) {
             const int n = *g.n_tokens, kept = g.hdr->kept;
             if (n > 0 && kept > 0) {
@@ -846,10 +860,15 @@ balance_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant
             const bool whole = MODE == kFwd && whole_pieces(p.p, row, p.M, p.N);
             const uint32_t apart = MODE == kFwd ? __ballot_sync(0xffffffffu, keep && !whole) : 0u;
             const float l_t = MODE == kGrid && keep ? g.token_loss[row] : 0.f;
-            // kGrads: the scales of ds and of the other operand, out again
-            const Pow2 out_scale(MODE == kGrads ? coef_exp + count_exp(g.hdr->most) - 15 -
-                                                      top_exp(p.a_mn ? g.hdr->x_top : g.hdr->w_top)
-                                                : 0);
+            // kGrid: ds / c to 2^14 at most, P's 2^14 out.  kGrads: the scales of ds
+            // (2^(13 - token_exp)) and of the other operand out again
+            const float row_scale = MODE == kGrid ? pow2f(-1 - token_exp(l_t)) : 1.f;
+            int out_exp = 0;
+            if (MODE == kGrads) {
+                out_exp = coef_exp - 27 - kNoExp + (p.a_mn ? g.hdr->x_top : g.hdr->w_top);
+                if (!p.a_mn && row < p.M) out_exp += token_exp(g.token_loss[row]);
+            }
+            const Pow2 out_scale(out_exp);
             float part = 0.f;
 #pragma unroll
             for (int q = 0; q < kEpiBlocks; ++q) {
@@ -876,8 +895,9 @@ balance_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant
                 } else {
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
-                        turn_buf[turned((int)lane, j)] =
-                            MODE == kGrads ? sum[q][j] * coef * out_scale.a * out_scale.b : sum[q][j];
+                        turn_buf[turned((int)lane, j)] = MODE == kGrads
+                            ? sum[q][j] * coef * out_scale.a * out_scale.b
+                            : (kUnscale * sum[q][j] - l_t) * row_scale;
                     __syncwarp();
                 }
                 if constexpr (MODE == kGrid) {
@@ -897,7 +917,6 @@ balance_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             const int r = r0 + 8 * (i2 + i);
-                            const float l = __shfl_sync(0xffffffffu, l_t, r);
                             const uint4 h4 = hi[i], l4 = lo[i];
                             const uint32_t wh[4] = {h4.x, h4.y, h4.z, h4.w}, wl[4] = {l4.x, l4.y, l4.z, l4.w};
                             uint32_t oh[4], ol[4];
@@ -905,10 +924,8 @@ balance_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant
                             for (int k = 0; k < 4; ++k) {
                                 const float2 ph = __half22float2(*reinterpret_cast<const __half2 *>(&wh[k]));
                                 const float2 pl = __half22float2(*reinterpret_cast<const __half2 *>(&wl[k]));
-                                const float a = (ph.x + pl.x) * scale1 *
-                                                (kUnscale * turn_buf[turned(r, c + 2 * k)] - l);
-                                const float b = (ph.y + pl.y) * scale1 *
-                                                (kUnscale * turn_buf[turned(r, c + 2 * k + 1)] - l);
+                                const float a = (ph.x + pl.x) * turn_buf[turned(r, c + 2 * k)];
+                                const float b = (ph.y + pl.y) * turn_buf[turned(r, c + 2 * k + 1)];
                                 const __half2 h = __floats2half2_rn(a, b);
                                 const float2 f = __half22float2(h);
                                 const __half2 o = __floats2half2_rn(a - f.x, b - f.y);
@@ -1209,12 +1226,13 @@ cudaError_t launch_balance_bwd(const uint16_t *x, const uint16_t *W_r, const uin
     BalPrep pp = {};
     pp.p_r = p_r; pp.p_c = p_c; pp.counts = counts; pp.mask = mask;
     pp.L = L; pp.N_r = N_r; pp.N_c = N_c; pp.d = d; pp.x = x; pp.W_r = W_r; pp.W_c = W_c;
+    pp.token_loss = token_loss;
     pp.T_hi = ws_at<uint16_t>(ws, w.T_hi);
     pp.T_lo = ws_at<uint16_t>(ws, w.T_lo);
     cudaError_t e = launch_prep(pp, ws, w, st);
     if (e != cudaSuccess) return e;
     BalCast ca = {};
-    ca.x = x; ca.W_r = W_r; ca.W_c = W_c; ca.mask = mask;
+    ca.x = x; ca.W_r = W_r; ca.W_c = W_c; ca.mask = mask; ca.token_loss = token_loss;
     ca.L = L; ca.N_r = N_r; ca.N_c = N_c; ca.d = d; ca.pr = pp.pr; ca.ld = w.ld;
     ca.x16 = ws_at<uint16_t>(ws, w.x16);
     ca.w16 = ws_at<uint16_t>(ws, w.w16);
@@ -1260,7 +1278,7 @@ cudaError_t launch_balance_bwd(const uint16_t *x, const uint16_t *W_r, const uin
     if ((e = launch_gemm<kGrid>(maps, g, st)) != cudaSuccess) return e;
 
     GemmArgs h = {};
-    h.hdr = pp.hdr; h.n_tokens = n_tokens;
+    h.hdr = pp.hdr; h.n_tokens = n_tokens; h.token_loss = token_loss;
     h.factor = (double)dloss * N_r * N_c / K;
     h.nprob = 2;
     const int nk_dw = (L + BK - 1) / BK, nk_dx = w.ld / BK;

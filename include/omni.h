@@ -366,11 +366,14 @@ int omni_expert_counts(const int32_t *idx, const uint8_t *mask, int L, int K, in
  *                       OMNI_DW_OVERWRITE, what they held is not read)
  *   x [L, d], W_r, W_c bf16 (the forward's; the rows of masked tokens of x do
  *   not matter); token_loss is the forward's.
- * Products run on the tensor cores with fp32 sums: exp(p) and ds enter as two
- * fp16 values each (hi + lo, 22 bits; exp(p) must stay below 4), x and W as
- * fp16 scaled by a power of two (exact for values down to 2^-32 of the largest
- * finite one, to 2^-39 of it below).  Every output element is written by one tile: the results are
- * the same on every run.
+ * Products run on the tensor cores with fp32 sums.  exp(p) and ds enter as two
+ * fp16 values each, hi + lo: 22 bits, down to 2^-39 of 1 for exp(p), which must
+ * stay below 3.99, and down to 2^-38 of c token_loss[t] for a token's ds, which
+ * that bounds (2^-98 c for smaller losses).  x and W enter as fp16 scaled by a
+ * power of two, exact for values down to 2^-32 of the largest finite one, to
+ * 2^-39 of it below; for dW_r and dW_c the rows of x count with token_loss[t] as
+ * a factor.  Every output element is written by one tile: the results are the
+ * same on every run.
  * ws: the size functions' bytes, 256-byte aligned.  dx, dW_r, dW_c, x, W_r,
  * W_c 16-byte aligned; dx, dW_r and dW_c share no memory (OMNI_ERR_INVALID_ARG).
  * d % 8 == 0.  Limits: N_r, N_c <= OMNI_MAX_AXIS, L <= 2^30.

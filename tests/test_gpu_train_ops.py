@@ -416,6 +416,36 @@ def test_balance_operands_of_any_magnitude(ex, ew, dloss):
     _check_balance_to_fp32(x, W_r, W_c, p_r, p_c, cnt["counts"], cnt["n_tokens"], 5, dloss=dloss)
 
 
+def _collapsed(L, N_r, N_c, K, spread, seed, d=64):
+    """All tokens on the same K experts, whatever their log-probabilities, whose
+    logits have this spread."""
+    g = _gen(seed)
+    x = torch.randn(L, d, generator=g, device=DEV).to(torch.bfloat16)
+    W_r, W_c = ((torch.randn(n, d, generator=g, device=DEV) * d ** -0.5).to(torch.bfloat16) for n in (N_r, N_c))
+    p_r, p_c = (torch.log_softmax(spread * torch.randn(L, n, generator=g, device=DEV), 1) for n in (N_r, N_c))
+    idx = (torch.arange(K, device=DEV) * (N_c + 1) % (N_r * N_c)).int().expand(L, K).contiguous()
+    cnt = omni.expert_counts(idx, N_r * N_c)
+    return x, W_r, W_c, p_r.contiguous(), p_c.contiguous(), cnt["counts"], cnt["n_tokens"]
+
+
+@pytest.mark.parametrize("L,N_r,N_c,K,spread", [(4096, 1304, 1304, 1, 0.01), (4096, 1304, 1304, 1, 1.0),
+                                                (2048, 1304, 1304, 64, 1.0), (512, 8192, 8192, 1, 0.01),
+                                                (512, 8192, 8192, 1, 1.0), (700, 8192, 40, 3, 3.0),
+                                                (3000, 257, 389, 1, 8.0)])
+def test_balance_of_a_collapsed_router(L, N_r, N_c, K, spread):
+    """Few experts take every task while the probabilities are spread over all:
+    the gradients are many powers of two below the largest count, and differ as
+    much between tokens.  Each token's dx is held to the bar by itself."""
+    x, W_r, W_c, p_r, p_c, counts, n = _collapsed(L, N_r, N_c, K, spread, L + K)
+    _, got, want = _check_balance_to_fp32(x, W_r, W_c, p_r, p_c, counts, n, K)
+    # a token's P are good to 2^-21 and 2^-39 of 1 each; l is a product of two
+    rows = want["dx"].norm(dim=1)
+    low = 2.0 ** -39 * (torch.exp(-p_r[:, :K].double().amin(1)) + torch.exp(-p_c.double()[:, (torch.arange(K) * (N_c + 1) % N_c)].amin(1)))
+    err = (got["dx"].double() - want["dx"]).norm(dim=1)
+    more = 2.0 ** -21 * want["dx_abs"].norm(dim=1)
+    assert (err <= (4 * BAR + 4 * low) * rows + more).all(), float((err / rows).max())
+
+
 # ------------------------------------------------------------------ norm
 def _rows(L, d, dtype, seed):
     g = _gen(seed)
