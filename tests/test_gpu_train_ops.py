@@ -357,19 +357,26 @@ def test_balance_counts_summed_over_replicas():
 
 # Bars that hold the balance gradients to fp32's accuracy, relative to the
 # results however small they are.  Rounding errors of single terms average out
-# of a norm; what stays is the tensor core's cutting off towards zero, 2^-24 of
-# the running sum at an instruction on average.  Over the 16 to 32 instructions
-# of an accumulator, whose sum grows as they go, that is 3e-7 to 6e-7 of a
-# product, and 2e-6 with four times as many: 1.5e-6 is asked for.  Where U and
-# l cancel, the errors of U and of l (2^-24 of themselves at a rounding each,
-# two of them) do not shrink with their difference: l's shifts a token's whole
-# row by 2^-23 c P l, U's are one by one (root of the sum of squares).
+# of a norm; what stays is the tensor core's cutting off towards zero, at most
+# 2^-23 of the running sum at an instruction and about half of that on average.
+# Over the 16 to 32 instructions of an accumulator, whose sum grows as they go,
+# that is 3e-7 to 6e-7 of a product of mixed signs, and 2e-6 with four times as
+# many: 1.5e-6 is asked for.
+# Where U and l cancel, their errors do not shrink with the difference.  U, V and
+# l are sums of positive terms, all cut off the same way: by up to 4.5 x 2^-23 in
+# accumulators of two K steps (8 instructions of hi halves, sum of 1/8 .. 8/8),
+# by up to 8.5 x 2^-23 in those of four, which hold two fifths of a sum at most:
+# 6.1 x 2^-23 in all.  l can lose less, by the place of its leading bits, so all
+# U - l and V - l of a token move by up to 6.1 x 2^-23 l.  Beside that, the terms'
+# own roundings (2^-24 each, of U, l and the difference) are 2^-23 one by one
+# (root of the sum of squares).
+SHIFT, EACH = 6.1 * 2.0 ** -23, 2.0 ** -23
 BAR = 1.5e-6
 
 
 def _cancelled(x, W_r, W_c, p_r, p_c, counts, n, K, dloss, mask):
-    """Norms behind dx, dW_r and dW_c where U and l cancel: of the shift by c P l
-    in each, and of the separate terms c P (U + l)."""
+    """What the errors of U and l leave in dx, dW_r and dW_c where they cancel:
+    norms of the shift by c P l, and of the separate terms c P (U + l)."""
     keep = torch.ones(len(x), dtype=torch.bool, device=DEV) if mask is None else mask.bool()
     Pr, Pc = (p[keep].double().exp() for p in (p_r, p_c))
     F = counts.double().reshape(Pr.shape[1], Pc.shape[1])
@@ -377,18 +384,19 @@ def _cancelled(x, W_r, W_c, p_r, p_c, counts, n, K, dloss, mask):
     tl = (Pr * U).sum(1, keepdim=True)
     c = abs(dloss) * F.numel() / (K * n * int(keep.sum()))
     xd, wr, wc = x[keep].double(), W_r.double(), W_c.double()
-    shift = dict(dx=c * tl * (Pr @ wr + Pc @ wc), dW_r=c * (Pr * tl).T @ xd, dW_c=c * (Pc * tl).T @ xd)
+    shift = dict(dx=(c * tl * (Pr @ wr)).norm() + (c * tl * (Pc @ wc)).norm(),
+                 dW_r=(c * (Pr * tl).T @ xd).norm(), dW_c=(c * (Pc * tl).T @ xd).norm())
     Ar, Ac = (c * Pr * (U + tl)).square(), (c * Pc * (V + tl)).square()
     each = dict(dx=Ar @ wr.square() + Ac @ wc.square(), dW_r=Ar.T @ xd.square(), dW_c=Ac.T @ xd.square())
-    return {k: float(shift[k].norm() + each[k].sum().sqrt()) for k in shift}
+    return {k: float(SHIFT * shift[k] + EACH * each[k].sum().sqrt()) for k in shift}
 
 
 def _check_balance_to_fp32(x, W_r, W_c, p_r, p_c, counts, n_tokens, K, dloss=1.0, mask=None, cancels=True):
-    """Gradients within BAR of their norm (with `cancels` also 2^-23 of what
-    cancels), every token's loss within 2^-18 of itself.  That is the sum of: 2^-20
-    cut off in 16 instructions at worst, over a growing sum; 2^-20 for the up to
-    150 additions after them (5 times the root of the sum of squares of 2^-24 each
-    uniformly); 2^-21 for exp and the halves of P, and 2^-22 for the other exp."""
+    """Gradients within BAR of their norm (with `cancels` also what _cancelled
+    gives), every token's loss within 2^-18 of itself.  That is the sum of: 4.5 x
+    2^-23 cut off; 2^-20 for the up to 150 additions after that (5 times the root
+    of the sum of squares of 2^-24 each, uniformly); 2^-21 for exp and the halves
+    of P, and 2^-22 for the other exp: 18.5 x 2^-23 in all, and 2^-18 is 32."""
     n = n_tokens.item()
     want = ref.balance_ref(x, W_r, W_c, p_r, p_c, counts, n, K, dloss, mask)
     fwd = omni.balance_fwd(p_r, p_c, counts, n_tokens, K, mask=mask)
@@ -399,7 +407,7 @@ def _check_balance_to_fp32(x, W_r, W_c, p_r, p_c, counts, n_tokens, K, dloss=1.0
     more = _cancelled(x, W_r, W_c, p_r, p_c, counts, n, K, dloss, mask) if cancels else {}
     for k in ("dx", "dW_r", "dW_c"):
         err, norm = float((got[k].double() - want[k]).norm()), float(want[k].norm())
-        assert norm > 0 and err <= BAR * norm + 2.0 ** -23 * more.get(k, 0.0), (k, err / norm)
+        assert norm > 0 and err <= BAR * norm + more.get(k, 0.0), (k, err / norm)
     return fwd, got, want
 
 
@@ -444,6 +452,57 @@ def test_balance_of_a_collapsed_router(L, N_r, N_c, K, spread):
     err = (got["dx"].double() - want["dx"]).norm(dim=1)
     more = 2.0 ** -21 * want["dx_abs"].norm(dim=1)
     assert (err <= (4 * BAR + 4 * low) * rows + more).all(), float((err / rows).max())
+
+
+def test_balance_headline_grid_to_fp32():
+    """What accumulators of two K steps are for: with eight, 2e-6 (the scale that
+    BAR is set against)."""
+    x, W_r, W_c, p_r, p_c, idx, _ = _balance_inputs(4096, 1024, 1304, 1304, 64, 31)
+    cnt = omni.expert_counts(idx, 1304 * 1304)
+    _check_balance_to_fp32(x, W_r, W_c, p_r, p_c, cnt["counts"], cnt["n_tokens"], 64, cancels=False)
+
+
+def _counts_past_2048(kind, N_r, N_c, g):
+    """Counts on a grid whose axes take several K steps: what fp16's rounding of
+    them leaves (none up to 2048) is a third product."""
+    few = torch.randint(0, 9, (N_r, N_c), generator=g, device=DEV, dtype=torch.int32)
+    if kind == "border":                                 # one count past 2048, in the last tile of both axes
+        few[N_r - 1, N_c - 1] = 2049
+    elif kind == "2048":                                 # none
+        few[N_r - 1, N_c - 1] = 2048
+    elif kind == "some":                                 # odd counts here and there
+        for i, j in ((0, 0), (N_r // 2, N_c - 1), (N_r - 1, N_c // 3)):
+            few[i, j] = 4097 + 2 * i + j
+    elif kind == "all":                                  # every one, up to 2^22
+        few = torch.randint(0, 1 << 22, (N_r, N_c), generator=g, device=DEV, dtype=torch.int32)
+        few[0, :3] = torch.tensor([(1 << 22) - 1, 1 << 22, 2049], dtype=torch.int32, device=DEV)
+    else:                                                # up to 2^31 - 1: to 22 bits
+        few = torch.randint(0, 1 << 30, (N_r, N_c), generator=g, device=DEV, dtype=torch.int32)
+        few[0, :3] = torch.tensor([(1 << 22) + 1, (1 << 31) - 1, 3], dtype=torch.int32, device=DEV)
+    return few.reshape(-1)
+
+
+@pytest.mark.parametrize("kind", ["border", "2048", "some", "all", "largest"])
+@pytest.mark.parametrize("L,N_r,N_c,masked", [(300, 257, 389, True),      # 5 and 7 K steps
+                                              (200, 300, 1100, False),    # 5 and 18
+                                              (260, 1304, 1000, False)])  # 21 and 16
+def test_balance_counts_past_2048(L, N_r, N_c, masked, kind):
+    """The product with the counts' remainders over several K steps, odd numbers
+    of them (its first step shares an accumulator with the last of the others),
+    several tiles, a lead of three and four steps."""
+    x, W_r, W_c, p_r, p_c, _, mask = _balance_inputs(L, 64, N_r, N_c, 1, L + N_r, masked)
+    counts = _counts_past_2048(kind, N_r, N_c, _gen(N_c))
+    n = torch.full((1,), 5000, dtype=torch.int32, device=DEV)
+    fwd, got, want = _check_balance_to_fp32(x, W_r, W_c, p_r, p_c, counts, n, 3, mask=mask)
+    # each expert by itself: tokens that are certain of one cell have its count as their loss
+    at = torch.tensor([[0, 0], [0, 1], [0, 2], [N_r // 2, N_c - 1], [N_r - 1, N_c // 3], [N_r - 1, N_c - 1]], device=DEV)
+    p_r, p_c = (torch.full((len(at), m), float("-inf"), device=DEV) for m in (N_r, N_c))
+    for k, p in enumerate((p_r, p_c)):
+        p[torch.arange(len(at), device=DEV), at[:, k]] = 0.0
+    sure = omni.balance_fwd(p_r, p_c, counts, n, 3)["token_loss"].double()
+    exact = counts[at[:, 0] * N_c + at[:, 1]].double()
+    assert torch.equal(sure[exact <= 1 << 22], exact[exact <= 1 << 22])
+    assert ((sure - exact).abs() <= 2.0 ** -22 * exact).all()
 
 
 # ------------------------------------------------------------------ norm
