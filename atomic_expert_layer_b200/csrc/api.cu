@@ -708,7 +708,7 @@ int omni_layer_norm_bwd(const void *x, const float *mean, const float *rstd, con
     return cuda_rc(launch_norm_bwd(x, (flags & OMNI_X_F32) != 0, mean, rstd, q, scale, w, dy, L, d,
                                    dx, (flags & OMNI_DX_ACCUMULATE) != 0, dw, db,
                                    (flags & OMNI_DW_OVERWRITE) != 0,
-                                   ws_at<float>(ws, sizeof(WsHeader)),
+                                   ws_at<float>(ws, sizeof(WsHeader)), ws_at<int>(ws, 0),
                                    reinterpret_cast<cudaStream_t>(stream)));
 }
 

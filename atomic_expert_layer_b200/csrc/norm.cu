@@ -406,14 +406,16 @@ norm_bwd_kernel(const T *__restrict__ x, const uint8_t *__restrict__ scale,
 }
 
 // dw, db += (or =) the sums of part[i][0], part[i][1] in a fixed order: 32
-// columns of a CTA, their rows in 32 slices.
+// columns of a CTA, their rows in 32 slices.  Clears the workspace's status word:
+// nothing here sets it.
 constexpr int kSumSlices = 32;
 __global__ void __launch_bounds__(32 * kSumSlices)
 norm_bwd_sum_kernel(const float *__restrict__ part, int nparts, int d, float *__restrict__ dw,
-                    float *__restrict__ db, int overwrite) {
+                    float *__restrict__ db, int overwrite, int *status) {
     __shared__ float sm[kSumSlices][33];
     grid_dependency_wait();
     grid_dependents_launch();
+    if (blockIdx.x == 0 && threadIdx.x == 0) *status = OMNI_DEV_OK;
     const int lane = (int)(threadIdx.x & 31), slice = (int)(threadIdx.x >> 5);
     const int c = blockIdx.x * 32 + lane;
     const int cols = db ? 2 * d : d;
@@ -558,7 +560,7 @@ cudaError_t launch_norm_fwd(const void *x, bool x_f32, const uint16_t *w, const 
 cudaError_t launch_norm_bwd(const void *x, bool x_f32, const float *mean, const float *rstd,
                             const uint8_t *q, const uint8_t *scale, const uint16_t *w,
                             const float *dy, int L, int d, float *dx, bool accumulate, float *dw,
-                            float *db, bool overwrite, float *part, cudaStream_t st) {
+                            float *db, bool overwrite, float *part, int *status, cudaStream_t st) {
     cudaError_t e;
     if (q)
         e = norm_bwd_t(q, scale, mean, rstd, w, dy, L, d, dx, accumulate, part, st);
@@ -571,7 +573,8 @@ cudaError_t launch_norm_bwd(const void *x, bool x_f32, const float *mean, const 
     if (e != cudaSuccess) return e;
     const int cols = db ? 2 * d : d;
     return launch(norm_bwd_sum_kernel, dim3((unsigned)((cols + 31) / 32)), dim3(32 * kSumSlices), 0,
-                  st, (const float *)part, norm_bwd_parts(L, d), d, dw, db, overwrite ? 1 : 0);
+                  st, (const float *)part, norm_bwd_parts(L, d), d, dw, db, overwrite ? 1 : 0,
+                  status);
 }
 
 cudaError_t launch_ckpt_pack(const void *x, bool x_f32, int L, int d, uint8_t *q, uint8_t *scale,

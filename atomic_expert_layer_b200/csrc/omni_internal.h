@@ -197,12 +197,12 @@ cudaError_t launch_norm_fwd(const void *x, bool x_f32, const uint16_t *w, const 
                             int d, float eps, uint16_t *y, float *mean, float *rstd, uint8_t *q,
                             uint8_t *scale, cudaStream_t st);
 // the kept rows are (q, scale) if q is not null, else (x, mean); db may be
-// null; part: norm_bwd_parts(L, d) rows of 2 d floats
+// null; part: norm_bwd_parts(L, d) rows of 2 d floats; clears the status word itself
 int norm_bwd_parts(int L, int d);
 cudaError_t launch_norm_bwd(const void *x, bool x_f32, const float *mean, const float *rstd,
                             const uint8_t *q, const uint8_t *scale, const uint16_t *w,
                             const float *dy, int L, int d, float *dx, bool accumulate, float *dw,
-                            float *db, bool overwrite, float *part, cudaStream_t st);
+                            float *db, bool overwrite, float *part, int *status, cudaStream_t st);
 cudaError_t launch_ckpt_pack(const void *x, bool x_f32, int L, int d, uint8_t *q, uint8_t *scale,
                              cudaStream_t st);
 // w (and then b) may be null

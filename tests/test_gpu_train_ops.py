@@ -661,6 +661,29 @@ def test_layer_norm_gradients_accumulate_and_repeat():
     assert torch.equal(got["dw"], one["dw"]) and torch.equal(got["db"], one["db"])
 
 
+@pytest.mark.parametrize("fill", [0, 0xff])
+def test_every_workspace_reports_its_own_call(fill):
+    """The status word that a caller reads afterwards is the call's, whatever the
+    workspace held: all of the operators that take one."""
+    L, d, N_r, N_c, K = 33, 256, 20, 30, 4
+    x, W_r, W_c, p_r, p_c, idx, _ = _balance_inputs(L, d, N_r, N_c, K, 4)
+    r, w, b, dy = _rows(L, d, torch.float32, 9)
+    W = V = torch.zeros(N_r * N_c, d, dtype=torch.bfloat16, device=DEV)
+    q, scale = omni.act_pack(x)
+    ws = lambda n: torch.full((n,), fill, dtype=torch.uint8, device=DEV)     # noqa: E731
+    used = [ws(256), ws(omni.omni_balance_fwd_workspace_size(L, N_r, N_c)),
+            ws(omni.omni_balance_bwd_workspace_size(L, d, N_r, N_c)), ws(omni.omni_layer_norm_bwd_workspace_size(L, d)),
+            ws(omni.omni_routed_bwd_ckpt_workspace_size(L, d, N_r, N_c, K))]
+    cnt = omni.expert_counts(idx, N_r * N_c, ws=used[0])
+    fwd = omni.balance_fwd(p_r, p_c, cnt["counts"], cnt["n_tokens"], K, ws=used[1])
+    omni.balance_bwd(x, W_r, W_c, p_r, p_c, cnt["counts"], cnt["n_tokens"], K, fwd["token_loss"], ws=used[2])
+    f = omni.layer_norm_fwd(r, w, b)
+    omni.layer_norm_bwd(dy, w, f["rstd"], x=r, mean=f["mean"], ws=used[3])
+    gate = torch.full((L, K), 1 / K, device=DEV)
+    omni.routed_bwd_ckpt(q, scale, W, V, W_r, W_c, idx, gate, dy, ws=used[4])
+    assert [omni.omni_get_device_status(t) for t in used] == [0] * 5
+
+
 def test_overwrite_does_not_read_the_gradients():
     """OMNI_DW_OVERWRITE on buffers full of NaN, through the C entry points."""
     L, d, N_r, N_c, K = 70, 256, 20, 30, 4
