@@ -93,10 +93,14 @@ __device__ __forceinline__ float block_max(float m) {        // of four neighbou
 // drops it and the conversion keeps it.  Infinities are looked for once a
 // block (testing every value made the kernel issue-bound: 75 us at L = 65536,
 // d = 2048, where 407 MB take 63).
-__device__ __forceinline__ uint2 ckpt_pack8(float *v, int *code) {
+__device__ __forceinline__ uint2 ckpt_pack8(const float *x, int *code) {
+    float v[8];
     float amax = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
+    for (int i = 0; i < 8; ++i) {
+        v[i] = x[i];
+        amax = fmaxf(amax, fabsf(v[i]));
+    }
     amax = block_max(amax);
     if (__any_sync(0xffffffffu, amax > 3.402823466e38f)) {
         amax = 0.f;

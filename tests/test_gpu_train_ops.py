@@ -578,6 +578,25 @@ def test_layer_norm_checkpoint(L, d, dtype):
     _within(got["db"], want["db"], adds * want["db_abs"] + 1e-30, "db")
 
 
+@pytest.mark.parametrize("d", [32, 96, 1024, 8192])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+def test_checkpoint_changes_nothing_where_the_norm_overflows(d, dtype):
+    """Rows whose variance is 0 in fp32 beside eps = 0, infinities and NaN: y with
+    a checkpoint is y without one, bit for bit (the checkpoint holds NaN)."""
+    x, w, b, _ = _rows(5, d, torch.float32, d)
+    x[1] *= 1e-30
+    x[2, d // 2] = float("inf")
+    x[3, 3] = float("nan")
+    x[4] = 0
+    x = x.to(dtype)
+    for bias in (b, None):
+        plain, out = (omni.layer_norm_fwd(x, w, bias, eps=0.0, ckpt=c) for c in (False, True))
+        assert torch.isinf(plain["y"][1].float()).any()  # (w has no zeros, x - mean hardly any)
+        for k in plain:
+            assert torch.equal(plain[k].nan_to_num(77.0, 88.0, -88.0), out[k].nan_to_num(77.0, 88.0, -88.0)), k
+        assert torch.equal(out["q"][1] & 127 == 127, ~torch.isfinite(plain["y"][1].float()))
+
+
 def test_layer_norm_against_differences():
     L, d, eps = 6, 64, 1e-5
     x, w, b, dy = _rows(L, d, torch.float32, 77)
