@@ -173,13 +173,17 @@ def shared_mlp_fwd(x, W_g, W_u, W_d, y=None, accumulate=False, ws=None, stream=N
 
 
 def layer_fwd(x, W, V, W_r, W_c, W_g, W_u, W_d, K, B, y=None, ws=None, mlp_ws=None,
-              stream=None, norm_w=None, norm_b=None, norm_eps=1e-5):
+              stream=None, norm_w=None, norm_b=None, norm_eps=None):
     """The whole layer: y = routed(x) + MLP(x), as omni_routed_fwd followed by
     omni_shared_mlp_fwd with OMNI_Y_ACCUMULATE on the same stream.  With norm_w
-    (and norm_b), x is the residual stream (bf16 or fp32) and the layer takes
-    its layer norm."""
+    (and norm_b, and norm_eps, 1e-5 where it is None), x is the residual stream
+    (bf16 or fp32) and the layer takes its layer norm; norm_b or norm_eps without
+    norm_w is a ValueError."""
     if norm_w is not None:
-        x = layer_norm_fwd(x, norm_w, norm_b, eps=norm_eps, stats=False, stream=stream)["y"]
+        eps = 1e-5 if norm_eps is None else norm_eps
+        x = layer_norm_fwd(x, norm_w, norm_b, eps=eps, stats=False, stream=stream)["y"]
+    elif norm_b is not None or norm_eps is not None:
+        raise ValueError("norm_b and norm_eps belong to a norm: norm_w is missing")
     y = routed_fwd(x, W, V, W_r, W_c, K, B, y=y, ws=ws, stream=stream)
     return shared_mlp_fwd(x, W_g, W_u, W_d, y=y, accumulate=True, ws=mlp_ws, stream=stream)
 

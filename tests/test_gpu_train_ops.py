@@ -871,6 +871,21 @@ def test_layer_fwd_with_its_norm():
     assert (got - want).norm() <= 1e-5 * want.norm()     # the expert sum's order varies between runs
 
 
+@pytest.mark.parametrize("L,dtype", [(1, torch.float32), (3, torch.bfloat16), (16, torch.float32), (17, torch.float32)])
+def test_layer_fwd_with_its_norm_on_few_tokens(L, dtype):
+    """Decode steps (the fused step up to 16 tokens) and the first size past them."""
+    cfg = configs.TINY
+    p = _layer_params(cfg, 3)
+    m = inputs.make_mlp_weights(cfg.d, configs.mlp_hidden(cfg.d), DEV, seed=3)
+    res = _rows(L, cfg.d, dtype, 4 + L)[0]
+    args = (p["W"], p["V"], p["W_r"], p["W_c"], m["W_g"], m["W_u"], m["W_d"], cfg.K, cfg.B)
+    for eps in (None, 1e-3):
+        n = omni.layer_norm_fwd(res, p["w"], p["b"], **({} if eps is None else dict(eps=eps)))["y"]
+        want = omni.layer_fwd(n, *args)
+        got = omni.layer_fwd(res, *args, norm_w=p["w"], norm_b=p["b"], norm_eps=eps)
+        assert (got - want).norm() <= 1e-5 * want.norm()
+
+
 # ----------------------------------------------- streams, graphs, workspaces
 def _flat(s):
     return {k: v.clone() for k, v in s.items()}

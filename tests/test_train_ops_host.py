@@ -255,6 +255,13 @@ def test_routed_bwd_refuses_misaligned_routing(lib, at):
     assert lib.omni_routed_bwd(*bwd) == -1
 
 
+def test_layer_fwd_refuses_half_a_norm(lib):
+    x, w = torch.zeros(4, 256, dtype=torch.bfloat16), torch.ones(256, dtype=torch.bfloat16)
+    for given in (dict(norm_b=w), dict(norm_eps=1e-6), dict(norm_b=w, norm_eps=0.0)):
+        with pytest.raises(ValueError, match="norm_w is missing"):
+            omni.layer_fwd(x, x, x, x, x, x, x, x, 2, 32, **given)
+
+
 def test_wrappers_refuse_cpu_tensors(lib):
     x = torch.zeros(4, 64, dtype=torch.bfloat16)
     w = torch.zeros(64, dtype=torch.bfloat16)
