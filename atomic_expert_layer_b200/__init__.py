@@ -178,14 +178,20 @@ def layer_fwd(x, W, V, W_r, W_c, W_g, W_u, W_d, K, B, y=None, ws=None, mlp_ws=No
     omni_shared_mlp_fwd with OMNI_Y_ACCUMULATE on the same stream.  With norm_w
     (and norm_b, and norm_eps, 1e-5 where it is None), x is the residual stream
     (bf16 or fp32) and the layer takes its layer norm; norm_b or norm_eps without
-    norm_w is a ValueError."""
+    norm_w is a ValueError.  What it allocates belongs to the stream it runs on
+    (`stream`, or the current one)."""
+    if stream is not None:
+        # all of its scratch is released when it returns, while the stream still runs
+        with torch.cuda.stream(stream):
+            return layer_fwd(x, W, V, W_r, W_c, W_g, W_u, W_d, K, B, y, ws, mlp_ws, None, norm_w,
+                             norm_b, norm_eps)
     if norm_w is not None:
         eps = 1e-5 if norm_eps is None else norm_eps
-        x = layer_norm_fwd(x, norm_w, norm_b, eps=eps, stats=False, stream=stream)["y"]
+        x = layer_norm_fwd(x, norm_w, norm_b, eps=eps, stats=False)["y"]
     elif norm_b is not None or norm_eps is not None:
         raise ValueError("norm_b and norm_eps belong to a norm: norm_w is missing")
-    y = routed_fwd(x, W, V, W_r, W_c, K, B, y=y, ws=ws, stream=stream)
-    return shared_mlp_fwd(x, W_g, W_u, W_d, y=y, accumulate=True, ws=mlp_ws, stream=stream)
+    y = routed_fwd(x, W, V, W_r, W_c, K, B, y=y, ws=ws)
+    return shared_mlp_fwd(x, W_g, W_u, W_d, y=y, accumulate=True, ws=mlp_ws)
 
 
 # ------------------------------------------------------- training operators

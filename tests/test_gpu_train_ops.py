@@ -921,6 +921,27 @@ def test_calls_on_two_streams_at_once():
                 assert torch.equal(w_[k], g_[k]), k
 
 
+@pytest.mark.parametrize("norm", [False, True])
+def test_layer_fwd_on_a_stream_keeps_its_scratch(norm):
+    """The call returns while its stream is still busy; what is allocated and
+    written on the current stream meanwhile is none of its scratch."""
+    cfg = configs.TINY
+    p = _layer_params(cfg, 3)
+    m = inputs.make_mlp_weights(cfg.d, configs.mlp_hidden(cfg.d), DEV, seed=3)
+    res = _rows(cfg.L, cfg.d, torch.bfloat16, 8)[0]
+    args = (p["W"], p["V"], p["W_r"], p["W_c"], m["W_g"], m["W_u"], m["W_d"], cfg.K, cfg.B)
+    given = dict(norm_w=p["w"], norm_b=p["b"]) if norm else {}
+    want = omni.layer_fwd(res, *args, **given)
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(20_000_000)
+    got = omni.layer_fwd(res, *args, **given, stream=stream)
+    over = [torch.zeros(n, dtype=torch.uint8, device=DEV) for n in (1 << k for k in range(9, 25)) for _ in range(4)]
+    torch.cuda.synchronize()
+    assert (got - want).norm() <= 1e-5 * want.norm() and not any(t.any() for t in over)
+
+
 def test_captured_and_replayed():
     """The chain in a CUDA graph, replayed on new inputs in the same buffers; a
     second graph that shares the workspaces, replayed in turn with the first."""
