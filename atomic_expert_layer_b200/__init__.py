@@ -242,6 +242,14 @@ def _bf16_or_f32(name, t, shape, di):
     return _at(name, t, _BF16, shape, di), 0
 
 
+def _number(name, v):
+    """v as a Python number.  A CUDA tensor is read back, which waits for its
+    stream and cannot be captured."""
+    if isinstance(v, torch.Tensor) and v.is_cuda and torch.cuda.is_current_stream_capturing():
+        raise ValueError(f"{name}: a Python number is expected while a graph is captured")
+    return float(v)
+
+
 def _mask_at(mask, L, di):
     if mask is None:
         return None
@@ -344,13 +352,16 @@ def balance_bwd(x, W_r, W_c, p_r, p_c, counts, n_tokens, K, token_loss, dloss=1.
                 dx=None, dW_r=None, dW_c=None, ws=None, stream=None):
     """Gradients of dloss * balance loss.  With a given dx the gradient is
     added to it (routed_bwd's dx), else a new one is returned; dW_r, dW_c are
-    accumulated into the given fp32 buffers (new ones if None)."""
+    accumulated into the given fp32 buffers (new ones if None).  dloss is a
+    number of the host: one on the device is read back first, so the call waits
+    for it (and refuses it while a graph is captured)."""
     L, d, di = _rows("x", x)
     N_r, N_c = _rows("W_r", W_r)[0], _rows("W_c", W_c)[0]
     if _elsewhere(di, stream):
         with _on(di, stream):
             return balance_bwd(x, W_r, W_c, p_r, p_c, counts, n_tokens, K, token_loss, dloss, mask,
                                dx, dW_r, dW_c, ws)
+    dloss = _number("dloss", dloss)
     at = (_at("x", x, _BF16, (L, d), di), _at("W_r", W_r, _BF16, (N_r, d), di),
           _at("W_c", W_c, _BF16, (N_c, d), di), _at("p_r", p_r, _F32, (L, N_r), di),
           _at("p_c", p_c, _F32, (L, N_c), di), _at("counts", counts, _I32, (N_r * N_c,), di),
@@ -365,7 +376,7 @@ def balance_bwd(x, W_r, W_c, p_r, p_c, counts, n_tokens, K, token_loss, dloss=1.
     lib = load()
     ws, ws_at, ws_n = _scratch(ws, lib.omni_balance_bwd_workspace_size(L, d, N_r, N_c), di)
     _check("omni_balance_bwd", lib.omni_balance_bwd(
-        *at, L, d, N_r, N_c, K, float(dloss), dx.data_ptr(), dW_r.data_ptr(), dW_c.data_ptr(), flags,
+        *at, L, d, N_r, N_c, K, dloss, dx.data_ptr(), dW_r.data_ptr(), dW_c.data_ptr(), flags,
         ws_at, ws_n, _queue(di)))
     return dict(dx=dx, dW_r=dW_r, dW_c=dW_c)
 

@@ -994,6 +994,27 @@ def test_captured_and_replayed():
             assert torch.equal(out[k], want[at][k]), (turn, k)
 
 
+def test_dloss_on_the_device():
+    """Read back outside a capture; refused in one, which goes on without harm."""
+    L, d, N_r, N_c, K = 50, 64, 12, 20, 3
+    x, W_r, W_c, p_r, p_c, idx, _ = _balance_inputs(L, d, N_r, N_c, K, 5)
+    cnt = omni.expert_counts(idx, N_r * N_c)
+    fwd = omni.balance_fwd(p_r, p_c, cnt["counts"], cnt["n_tokens"], K)
+    args = (x, W_r, W_c, p_r, p_c, cnt["counts"], cnt["n_tokens"], K, fwd["token_loss"])
+    want = omni.balance_bwd(*args, dloss=0.25)
+    scale = torch.tensor(0.25, device=DEV)
+    got = omni.balance_bwd(*args, dloss=scale)
+    assert all(torch.equal(got[k], want[k]) for k in want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(ValueError, match="dloss"):
+            omni.balance_bwd(*args, dloss=scale)
+        got = omni.balance_bwd(*args, dloss=0.25)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(got[k], want[k]) for k in want)
+
+
 def test_wrappers_refuse_what_does_not_fit():
     x, w, b, dy = _rows(4, 64, torch.float32, 1)
     f = omni.layer_norm_fwd(x, w, b)
