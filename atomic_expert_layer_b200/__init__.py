@@ -225,10 +225,19 @@ def _at(name, t, dtype, shape, di):
     _refuse(name, t, dtype, shape, di)
 
 
+def _size(name, n):
+    """n as the C entry points take it; they would see a larger one modulo 2^32."""
+    if not n < 1 << 31:
+        raise ValueError(f"{name}: {n} is not below 2^31")
+    return n
+
+
 def _rows(name, t):
     """Shape [rows, columns] and device index of a CUDA matrix."""
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
         raise ValueError(f"{name}: a tensor of 2 dimensions is expected")
+    if t.numel() >= 1 << 31:
+        _size(name, max(t.shape))
     di = t.get_device()
     if di < 0:
         raise ValueError(f"{name}: a CUDA tensor is expected")
@@ -317,6 +326,7 @@ def expert_counts(idx, N, mask=None, ws=None, stream=None):
     """Tasks per expert and kept tokens: counts [N] and n_tokens [1], int32.
     idx [L, K] int32; mask [L] bool or uint8, None = every token counts."""
     L, K, di = _rows("idx", idx)
+    _size("N", N)
     if _elsewhere(di, stream):
         with _on(di, stream):
             return expert_counts(idx, N, mask, ws)
@@ -334,6 +344,7 @@ def balance_fwd(p_r, p_c, counts, n_tokens, K, mask=None, ws=None, stream=None):
     expert_counts."""
     L, N_r, di = _rows("p_r", p_r)
     N_c = _rows("p_c", p_c)[1]
+    _size("K", K)
     if _elsewhere(di, stream):
         with _on(di, stream):
             return balance_fwd(p_r, p_c, counts, n_tokens, K, mask, ws)
@@ -357,6 +368,7 @@ def balance_bwd(x, W_r, W_c, p_r, p_c, counts, n_tokens, K, token_loss, dloss=1.
     for it (and refuses it while a graph is captured)."""
     L, d, di = _rows("x", x)
     N_r, N_c = _rows("W_r", W_r)[0], _rows("W_c", W_c)[0]
+    _size("K", K)
     if _elsewhere(di, stream):
         with _on(di, stream):
             return balance_bwd(x, W_r, W_c, p_r, p_c, counts, n_tokens, K, token_loss, dloss, mask,

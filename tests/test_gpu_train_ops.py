@@ -994,6 +994,18 @@ def test_captured_and_replayed():
             assert torch.equal(out[k], want[at][k]), (turn, k)
 
 
+@pytest.mark.parametrize("n", [1 << 31, (1 << 32) + 64])
+def test_wrappers_refuse_numbers_past_31_bits(n):
+    idx = torch.zeros(4, 2, dtype=torch.int32, device=DEV)
+    p = torch.zeros(4, 8, device=DEV)
+    W, x = torch.zeros(8, 64, dtype=torch.bfloat16, device=DEV), torch.zeros(4, 64, dtype=torch.bfloat16, device=DEV)
+    cnt = omni.expert_counts(idx, 64)
+    for call in (lambda: omni.expert_counts(idx, n), lambda: omni.balance_fwd(p, p, cnt["counts"], cnt["n_tokens"], n),
+                 lambda: omni.balance_bwd(x, W, W, p, p, cnt["counts"], cnt["n_tokens"], n, p[:, 0].contiguous())):
+        with pytest.raises(ValueError, match="not below 2\\^31"):
+            call()
+
+
 def test_dloss_on_the_device():
     """Read back outside a capture; refused in one, which goes on without harm."""
     L, d, N_r, N_c, K = 50, 64, 12, 20, 3

@@ -255,6 +255,21 @@ def test_routed_bwd_refuses_misaligned_routing(lib, at):
     assert lib.omni_routed_bwd(*bwd) == -1
 
 
+@pytest.mark.parametrize("n", [1 << 31, (1 << 32) + 3])
+def test_wrappers_refuse_sizes_past_31_bits(lib, n):
+    """The C entry points take sizes of 32 bits: 2^32 + 3 rows would run as 3."""
+    def rows(dtype, columns):
+        return torch.zeros(1, columns, dtype=dtype).expand(n, columns)
+
+    bf, f, u = rows(torch.bfloat16, 64), rows(torch.float32, 64), rows(torch.uint8, 64)
+    w, i = torch.zeros(64, dtype=torch.bfloat16), rows(torch.int32, 1)
+    for call in (lambda: omni.layer_norm_fwd(bf, w), lambda: omni.layer_norm_bwd(f, w, f[:, 0], x=f, mean=f[:, 0]),
+                 lambda: omni.act_pack(bf), lambda: omni.act_unpack(u, u[:, :2]), lambda: omni.expert_counts(i, 16),
+                 lambda: omni.balance_fwd(f, f, i, i, 2)):
+        with pytest.raises(ValueError, match="not below 2\\^31"):
+            call()
+
+
 def test_layer_fwd_refuses_half_a_norm(lib):
     x, w = torch.zeros(4, 256, dtype=torch.bfloat16), torch.ones(256, dtype=torch.bfloat16)
     for given in (dict(norm_b=w), dict(norm_eps=1e-6), dict(norm_b=w, norm_eps=0.0)):
