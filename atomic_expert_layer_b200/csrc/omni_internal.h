@@ -192,7 +192,7 @@ cudaError_t launch_shared_mlp(const uint16_t *x, const uint16_t *W_g, const uint
                               bool accumulate, int *status, cudaStream_t st);
 
 // ---- layer norm and 8-bit activation checkpoints (norm.cu)
-// mean, rstd, q / scale (together) and y may be null
+// mean, rstd, b and q / scale (together) may be null
 cudaError_t launch_norm_fwd(const void *x, bool x_f32, const uint16_t *w, const uint16_t *b, int L,
                             int d, float eps, uint16_t *y, float *mean, float *rstd, uint8_t *q,
                             uint8_t *scale, cudaStream_t st);
