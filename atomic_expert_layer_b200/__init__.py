@@ -324,7 +324,9 @@ def _grads(names, given, like):
 
 def expert_counts(idx, N, mask=None, ws=None, stream=None):
     """Tasks per expert and kept tokens: counts [N] and n_tokens [1], int32.
-    idx [L, K] int32; mask [L] bool or uint8, None = every token counts."""
+    idx [L, K] int32; mask [L] bool or uint8, None = every token counts.  Ids
+    outside [0, N) are not counted; omni_get_device_status of the workspace, which
+    is returned as ws, reports them."""
     L, K, di = _rows("idx", idx)
     _size("N", N)
     if _elsewhere(di, stream):
@@ -335,7 +337,7 @@ def expert_counts(idx, N, mask=None, ws=None, stream=None):
     _check("omni_expert_counts", load().omni_expert_counts(
         _at("idx", idx, _I32, (L, K), di), _mask_at(mask, L, di), L, K, N, counts.data_ptr(),
         n_tokens.data_ptr(), ws_at, ws_n, _queue(di)))
-    return dict(counts=counts, n_tokens=n_tokens)
+    return dict(counts=counts, n_tokens=n_tokens, ws=ws)
 
 
 def balance_fwd(p_r, p_c, counts, n_tokens, K, mask=None, ws=None, stream=None):

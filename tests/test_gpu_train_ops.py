@@ -93,6 +93,18 @@ def test_expert_counts_reports_a_bad_id_and_counts_the_rest():
     assert none["n_tokens"].item() == 0 and not none["counts"].any()
 
 
+@pytest.mark.parametrize("bad", [-1, 16, 1 << 30])
+def test_expert_counts_keeps_its_status(bad):
+    """A bad id is found out without a workspace of the caller's."""
+    idx = torch.tensor([[0, 5], [3, 3]], dtype=torch.int32, device=DEV)
+    assert omni.omni_get_device_status(omni.expert_counts(idx, 16)["ws"]) == 0
+    idx[1, 0] = bad
+    out = omni.expert_counts(idx, 16)
+    assert omni.omni_get_device_status(out["ws"]) == 1 and int(out["counts"].sum()) == 3
+    ws = torch.empty(512, dtype=torch.uint8, device=DEV)
+    assert omni.expert_counts(idx, 16, ws=ws)["ws"] is ws and omni.omni_get_device_status(ws) == 1
+
+
 # --------------------------------------------------------------- balance
 def _balance_inputs(L, d, N_r, N_c, K, seed, masked=False, hot=False):
     """Log-probabilities of a router on random tokens; hot: all tokens on a few
