@@ -715,6 +715,50 @@ def test_every_workspace_reports_its_own_call(fill):
     assert [omni.omni_get_device_status(t) for t in used] == [0] * 5
 
 
+def test_bindings_give_what_the_wrappers_give():
+    """The omni_* bindings with buffers of the caller's, bit for bit (the routed
+    backward's atomics aside), and what their outputs leave alone."""
+    L, d, N_r, N_c, K = 33, 256, 20, 30, 4
+    x, W_r, W_c, p_r, p_c, idx, mask = _balance_inputs(L, d, N_r, N_c, K, 4, masked=True)
+    r, w, b, dy = _rows(L, d, torch.float32, 9)
+    new = lambda t: torch.full_like(t, 7)                # noqa: E731
+    ws = torch.empty(1 << 24, dtype=torch.uint8, device=DEV)
+
+    def same(got, want):
+        for g, v in zip(got, want):
+            assert torch.equal(g, v)
+
+    c = omni.expert_counts(idx, N_r * N_c, mask=mask)
+    out = new(c["counts"]), new(c["n_tokens"])
+    omni.omni_expert_counts(idx, mask, L, K, N_r * N_c, *out, ws)
+    same(out, (c["counts"], c["n_tokens"]))
+    f = omni.balance_fwd(p_r, p_c, c["counts"], c["n_tokens"], K, mask=mask)
+    out = new(f["loss"]), new(f["token_loss"])
+    omni.omni_balance_fwd(p_r, p_c, c["counts"], c["n_tokens"], mask, L, N_r, N_c, K, *out, ws)
+    same(out, (f["loss"], f["token_loss"]))
+    n = omni.layer_norm_fwd(r, w, b, ckpt=True)
+    out = [new(n[k]) for k in ("y", "mean", "rstd", "q", "scale")]
+    omni.omni_layer_norm_fwd(r, w, b, L, d, 1e-5, *out, omni.OMNI_X_F32)
+    same(out, [n[k] for k in ("y", "mean", "rstd", "q", "scale")])
+    packed = omni.act_pack(x)
+    out = [new(t) for t in packed]
+    omni.omni_act_pack(x, L, d, *out, 0)
+    same(out, packed)
+    y = new(x)
+    omni.omni_act_unpack(*packed, w, b, L, d, y)
+    same([y], [omni.act_unpack(*packed, w, b)])
+    W, V = ((torch.randn(N_r * N_c, d, generator=_gen(s), device=DEV) * 0.1).to(torch.bfloat16) for s in (1, 2))
+    gate = torch.full((L, K), 1 / K, device=DEV)
+    g = omni.routed_bwd_ckpt(*packed, W, V, W_r, W_c, idx, gate, dy, w=w, b=b)
+    names = ("dx", "dW", "dV", "dW_r", "dW_c")
+    for flags, start in ((0, 1.0), (omni.OMNI_DW_OVERWRITE, float("nan"))):
+        out = [torch.full_like(g[k], start) for k in names]
+        omni.omni_routed_bwd_ckpt(*packed, w, b, W, V, W_r, W_c, L, d, N_r, N_c, K, idx, gate, dy, *out, flags, ws)
+        for k, t in zip(names, out):
+            base = start if flags == 0 and k != "dx" else 0.0
+            assert (t - base - g[k]).norm() <= 1e-5 * (g[k].norm() + base * g[k].numel() ** 0.5), k
+
+
 def test_overwrite_does_not_read_the_gradients():
     """OMNI_DW_OVERWRITE on buffers full of NaN, through the C entry points."""
     L, d, N_r, N_c, K = 70, 256, 20, 30, 4
