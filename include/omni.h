@@ -365,7 +365,7 @@ int omni_expert_counts(const int32_t *idx, const uint8_t *mask, int L, int K, in
  *   dW_r [N_r, d], dW_c [N_c, d] fp32  += ds^T x, accumulated (= with
  *                       OMNI_DW_OVERWRITE, what they held is not read)
  *   x [L, d], W_r, W_c bf16 (the forward's; the rows of masked tokens of x do
- *   not matter); token_loss is the forward's.
+ *   not matter); token_loss is the forward's, of the same p, counts and mask.
  * Products run on the tensor cores with fp32 sums.  exp(p) and ds enter as two
  * fp16 values each, hi + lo: 22 bits, down to 2^-39 of 1 for exp(p), which must
  * stay below 3.99, and down to 2^-38 of c token_loss[t] for a token's ds, which

@@ -466,6 +466,42 @@ def test_balance_of_a_collapsed_router(L, N_r, N_c, K, spread):
     assert (err <= (4 * BAR + 4 * low) * rows + more).all(), float((err / rows).max())
 
 
+@pytest.mark.parametrize("top", [1.0, 2.5, 3.98])
+@pytest.mark.parametrize("count", [1, 1023, 1025, 2047])
+def test_balance_probabilities_up_to_their_limit(top, count):
+    """exp(p) may be anything below 3.99, normalised or not: ds stays in range,
+    at counts on both sides of a power of two."""
+    L, N_r, N_c = 70, 65, 130
+    x, W_r, W_c, p_r, p_c, _, _ = _balance_inputs(L, 64, N_r, N_c, 1, 17)
+    for p in (p_r, p_c):
+        p[:, 3] = np.log(top)
+        p[::3, 5] = np.log(top)
+    counts = torch.zeros(N_r, N_c, dtype=torch.int32, device=DEV)
+    counts[3, 3] = counts[5, 3] = counts[40, 100] = count
+    n = torch.full((1,), 4000, dtype=torch.int32, device=DEV)
+    _check_balance_to_fp32(x, W_r, W_c, p_r, p_c, counts.reshape(-1), n, 1)
+
+
+def test_balance_a_token_without_numbers():
+    """NaN in one token's probabilities reaches its own dx and the weights'
+    gradients, and nothing else."""
+    L, d, N_r, N_c, K = 90, 64, 30, 50, 4
+    x, W_r, W_c, p_r, p_c, idx, _ = _balance_inputs(L, d, N_r, N_c, K, 12)
+    cnt = omni.expert_counts(idx, N_r * N_c)
+
+    def step():
+        f = omni.balance_fwd(p_r, p_c, cnt["counts"], cnt["n_tokens"], K)
+        return {**f, **omni.balance_bwd(x, W_r, W_c, p_r, p_c, cnt["counts"], cnt["n_tokens"], K, f["token_loss"])}
+
+    clean = step()
+    p_r[17, 4] = float("nan")
+    got = step()
+    rest = torch.arange(L, device=DEV) != 17
+    for k in ("token_loss", "dx"):
+        assert torch.equal(got[k][rest], clean[k][rest]) and torch.isnan(got[k][17]).all()
+    assert all(torch.isnan(got[k]).all() for k in ("loss", "dW_r", "dW_c"))
+
+
 def test_balance_headline_grid_to_fp32():
     """What accumulators of two K steps are for: with eight, 2e-6 (the scale that
     BAR is set against)."""
