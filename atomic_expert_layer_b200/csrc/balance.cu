@@ -32,9 +32,15 @@
 //     magnitude becomes 2^14 to 2^15.  fp16 then holds every bf16 value down to
 //     2^-32 of it exactly.
 // bf16 halves (16 bits) need no scales, but left dx and dW off by 2.9e-6 of
-// themselves, and by 4e-3 for a collapsed router, where U - l_t cancels.  With
-// these, and with what kChunk below says, the results are as near to 64 bits
-// as fp32 arithmetic's (headline: 5e-7, torch in fp32 1.2e-6).
+// themselves, and by 4e-3 for a collapsed router, where U - l_t cancels.  A
+// scale of ds by the largest count left 6e-5 at 1304 x 1304 and 1e-2 at 8192 x
+// 8192 where spread probabilities meet tasks on one expert.  With these, and
+// with what kChunk below says, the gradients' errors against 64 bits are near
+// those of torch in fp32, a little above or below by the inputs: headline
+// 5.6e-7 and 1.2e-6, skewed layer 1.3e-6 to 2.3e-6 and 2.0e-6 to 2.7e-6 (four
+// seeds).  They are up to twice torch's where U and l agree in all but their
+// last bits (counts of millions on every expert: 3.5e-5 and 1.7e-5), since both
+// are cut off towards zero, by different amounts.
 //
 // Bounds and measurements, headline layer (L = 4096, d = 1024, 1304 x 1304
 // grid, one B200, clocks under load): the products are 28 GFLOP forward, 56 +
@@ -504,7 +510,8 @@ constexpr int kMaxProbs = 2, kMaxMaps = 6;
 // small, then the 8 of the hi halves; the additions in registers round to
 // nearest.  Headline step, and largest error against 64 bits there and at the
 // skewed layer: 2 steps 266 us, 5e-7, 1.3e-6; 4 steps 248 us, 7e-7, 2.9e-6; 8
-// steps, halves together, 227 us, 2e-6, 5.6e-6 (torch in fp32: 1.2e-6, 2.7e-6).
+// steps, halves together, 227 us, 2e-6, 5.6e-6 (torch in fp32: 1.2e-6, 2.0e-6
+// to 2.7e-6 by the seed).
 // A backward tile's first two accumulators take up to kMaxLead steps (a fifth
 // of them at most): they are computed while the warps that would drain them
 // still write the last tile (headline step 265 -> 258 us; with 8 steps and a
@@ -596,9 +603,11 @@ __device__ __forceinline__ int chunk_steps(const GemmProb &p, int st, int steps)
 }
 
 // Arrive on the pair's first CTA's barrier.  What it orders are TMEM reads,
-// which have completed; at cluster scope (and with acquires at cluster scope
-// on the other side) each arrive would also wait for the warp's global stores,
-// and each wait drop the SM's L1.
+// which have completed (tcgen05.wait::ld, then the fence before thread
+// synchronisation; the issuer fences after its wait); no other memory that one
+// CTA writes is read by the other.  At cluster scope (and with acquires at
+// cluster scope on the other side) each arrive would also wait for the warp's
+// global stores, and each wait drop the SM's L1.
 __device__ __forceinline__ void mbar_arrive_pair(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -1155,7 +1164,12 @@ cudaError_t launch_counts(const int32_t *idx, const uint8_t *mask, int64_t M, in
     if (e != cudaSuccess) return e;
     // crowded: as many tasks as experts or more, and enough of them for a CTA
     // on every SM (skewed layer, M = 2 N = 2^21: 17 against 61 us; with M = N =
-    // 2^18, 10 against 3)
+    // 2^18, 10 against 3).  The sizes stand for what decides, how many tasks meet
+    // on one expert, and are not always right.  In the table against one by one:
+    // even tasks, M = N = 2^20, 9.2 against 7.0 us, and M = 2 N, 12.9 against
+    // 11.6 (the table is taken); collapsed on 64 of 1304 x 1304 experts, 2^18
+    // tasks 6.0 against 11.1, 2^20 tasks 6.1 against 41, and 2^19 even tasks on
+    // 64 experts 7.3 against 133 (it is not).
     if (M >= N && M >= (int64_t)1 << 20)
         return launch(counts_crowded_kernel, dim3((unsigned)((M + kCrowdTasks - 1) / kCrowdTasks)),
                       dim3(kCrowdThreads), 0, st, idx, mask, (int)M, K, (int)N, counts, n_tokens, status);
