@@ -21,10 +21,16 @@ inline size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-// whether arrays of na and nb floats share memory
-bool overlap(const float *a, size_t na, const float *b, size_t nb) {
+// whether arrays of na and nb values share memory (null ones do not)
+template <typename A, typename B>
+bool overlap(const A *a, size_t na, const B *b, size_t nb) {
     const uintptr_t u = reinterpret_cast<uintptr_t>(a), v = reinterpret_cast<uintptr_t>(b);
-    return u < v + sizeof(float) * nb && v < u + sizeof(float) * na;
+    return a && b && u < v + sizeof(B) * nb && v < u + sizeof(A) * na;
+}
+// the same for n values at x, which is fp32 or bf16
+template <typename B>
+bool overlap_x(const void *x, bool x_f32, size_t n, const B *b, size_t nb) {
+    return overlap(static_cast<const uint8_t *>(x), n * (x_f32 ? 4 : 2), b, nb);
 }
 }  // namespace
 
@@ -602,6 +608,7 @@ int omni_expert_counts(const int32_t *idx, const uint8_t *mask, int L, int K, in
     if (!aligned4(idx) || !aligned4(counts) || !aligned4(n_tokens)) return OMNI_ERR_INVALID_ARG;
     const int rc = check_plain_ws(ws, ws_bytes, sizeof(WsHeader));
     if (rc) return rc;
+    if (overlap(counts, (size_t)N, idx, (size_t)L * K)) return OMNI_ERR_INVALID_ARG;
     first_launch_in_call();
     return cuda_rc(launch_counts(idx, mask, (int64_t)L * K, K, N, counts, n_tokens,
                                  ws_at<int>(ws, 0), reinterpret_cast<cudaStream_t>(stream)));
@@ -676,8 +683,13 @@ int omni_layer_norm_fwd(const void *x, const omni_bf16 *w, const omni_bf16 *b, i
     if (!aligned16(x) || !aligned16(w) || !aligned16(b) || !aligned16(y) || !aligned16(q) ||
         !aligned4(mean) || !aligned4(rstd))
         return OMNI_ERR_INVALID_ARG;
+    // each row is read before it is written, but not before the others are
+    const bool x_f32 = (flags & OMNI_X_F32) != 0;
+    const size_t n = (size_t)L * (size_t)d;
+    if ((overlap_x(x, x_f32, n, y, n) && (x_f32 || x != y)) || overlap_x(x, x_f32, n, q, n))
+        return OMNI_ERR_INVALID_ARG;
     first_launch_in_call();
-    return cuda_rc(launch_norm_fwd(x, (flags & OMNI_X_F32) != 0, w, b, L, d, eps, y, mean, rstd, q,
+    return cuda_rc(launch_norm_fwd(x, x_f32, w, b, L, d, eps, y, mean, rstd, q,
                                    scale, reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -704,8 +716,11 @@ int omni_layer_norm_bwd(const void *x, const float *mean, const float *rstd, con
     if (overlap(dx, nx, dw, nw) || (db && (overlap(dx, nx, db, nw) || overlap(dw, nw, db, nw))) ||
         (dx != dy && overlap(dx, nx, dy, nx)))
         return OMNI_ERR_INVALID_ARG;
+    const bool x_f32 = (flags & OMNI_X_F32) != 0;
+    if (q ? overlap(q, nx, dx, nx) : overlap_x(x, x_f32, nx, dx, nx) && !(x_f32 && x == dx))
+        return OMNI_ERR_INVALID_ARG;
     first_launch_in_call();
-    return cuda_rc(launch_norm_bwd(x, (flags & OMNI_X_F32) != 0, mean, rstd, q, scale, w, dy, L, d,
+    return cuda_rc(launch_norm_bwd(x, x_f32, mean, rstd, q, scale, w, dy, L, d,
                                    dx, (flags & OMNI_DX_ACCUMULATE) != 0, dw, db,
                                    (flags & OMNI_DW_OVERWRITE) != 0,
                                    ws_at<float>(ws, sizeof(WsHeader)), ws_at<int>(ws, 0),
@@ -718,8 +733,11 @@ int omni_act_pack(const void *x, int L, int d, uint8_t *q, uint8_t *scale, unsig
     if (rc) return rc;
     if ((flags & ~OMNI_X_F32) != 0 || !x || !q || !scale || !aligned16(x) || !aligned16(q))
         return OMNI_ERR_INVALID_ARG;
+    const bool x_f32 = (flags & OMNI_X_F32) != 0;
+    const size_t n = (size_t)L * (size_t)d;
+    if (overlap_x(x, x_f32, n, q, n)) return OMNI_ERR_INVALID_ARG;
     first_launch_in_call();
-    return cuda_rc(launch_ckpt_pack(x, (flags & OMNI_X_F32) != 0, L, d, q, scale,
+    return cuda_rc(launch_ckpt_pack(x, x_f32, L, d, q, scale,
                                     reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -728,7 +746,7 @@ int omni_act_unpack(const uint8_t *q, const uint8_t *scale, const omni_bf16 *w,
     const int rc = check_ckpt(L, d);
     if (rc) return rc;
     if (!q || !scale || !y || (b && !w) || !aligned16(q) || !aligned16(w) || !aligned16(b) ||
-        !aligned16(y))
+        !aligned16(y) || overlap(q, (size_t)L * (size_t)d, y, (size_t)L * (size_t)d))
         return OMNI_ERR_INVALID_ARG;
     first_launch_in_call();
     return cuda_rc(launch_ckpt_unpack(q, scale, w, b, L, d, y,

@@ -220,10 +220,11 @@ struct RawRow<uint8_t, VPT> {
 };
 
 // ---------------------------------------------------------------- forward
+// (y may be x, row for row)
 template <typename T, int G, int VPT, bool CKPT>
 __global__ void __launch_bounds__(cta_threads(G), fwd_ctas(G, VPT))
-norm_fwd_kernel(const T *__restrict__ x, const uint16_t *__restrict__ w,
-                const uint16_t *__restrict__ b, int L, int d, float eps, uint16_t *__restrict__ y,
+norm_fwd_kernel(const T *x, const uint16_t *__restrict__ w,
+                const uint16_t *__restrict__ b, int L, int d, float eps, uint16_t *y,
                 float *__restrict__ mean_out, float *__restrict__ rstd_out,
                 uint8_t *__restrict__ q, uint8_t *__restrict__ scale) {
     constexpr int GROUPS = cta_threads(G) / G;
@@ -298,10 +299,11 @@ norm_fwd_kernel(const T *__restrict__ x, const uint16_t *__restrict__ w,
 // --------------------------------------------------------------- backward
 // T: the kept rows' type, fp32 or bf16 with mean, or uint8_t for a checkpoint.
 // A CTA adds up dy xh and dy over its rows in registers, then over its groups
-// in shared memory, and writes them to part[blockIdx.x][2][d].
+// in shared memory, and writes them to part[blockIdx.x][2][d].  dx may be dy or x,
+// row for row.
 template <typename T, int G, int VPT>
 __global__ void __launch_bounds__(cta_threads(G), bwd_ctas(G, VPT))
-norm_bwd_kernel(const T *__restrict__ x, const uint8_t *__restrict__ scale,
+norm_bwd_kernel(const T *x, const uint8_t *__restrict__ scale,
                 const float *__restrict__ mean_in, const float *__restrict__ rstd_in,
                 const uint16_t *__restrict__ w, const float *dy, int L, int d, float *dx,
                 int accumulate, float *__restrict__ part) {

@@ -330,8 +330,8 @@ int omni_shared_mlp_fwd(const omni_bf16 *x, const omni_bf16 *W_g, const omni_bf1
  * idx [L, K] int32 (omni_router_topk's); mask [L] bytes, NULL = every token
  * counts (padding tokens have mask 0; their ids are not read).  Both outputs
  * are overwritten and do not depend on the order of the atomics.  An id
- * outside [0, N) sets OMNI_DEV_BAD_EXPERT and is not counted.  ws: at least
- * 256 bytes.  With several replicas, the counts and n_tokens may be summed
+ * outside [0, N) sets OMNI_DEV_BAD_EXPERT and is not counted.  counts and idx
+ * share no memory.  ws: at least 256 bytes.  With several replicas, the counts and n_tokens may be summed
  * over the replicas before the balance calls.  Limits: L * K and N < 2^31.
  */
 int omni_expert_counts(const int32_t *idx, const uint8_t *mask, int L, int K, int N,
@@ -400,7 +400,8 @@ int omni_balance_bwd(const omni_bf16 *x, const omni_bf16 *W_r, const omni_bf16 *
  *   q [L, d], scale [L, d / 32] bytes: optional outputs (both or neither), the
  *   8-bit checkpoint of xh (omni_act_pack's form); d % 32 == 0 with them.
  * eps >= 0 (a constant row has xh = 0 with eps > 0).  d % 8 == 0,
- * d <= OMNI_MAX_NORM_D.  Arrays 16-byte aligned (mean, rstd 4, scale 1).
+ * d <= OMNI_MAX_NORM_D.  Arrays 16-byte aligned (mean, rstd 4, scale 1).  y may
+ * be a bf16 x; any other y or q that shares memory with x is refused.
  */
 int omni_layer_norm_fwd(const void *x, const omni_bf16 *w, const omni_bf16 *b, int L, int d,
                         float eps, omni_bf16 *y, float *mean, float *rstd, uint8_t *q,
@@ -415,7 +416,8 @@ int omni_layer_norm_fwd(const void *x, const omni_bf16 *w, const omni_bf16 *b, i
  *   (with the flag: dy plus the gradient, what a residual around the norm alone
  *   passes on)
  *   dw [d], db [d] fp32  accumulated (+=; = with OMNI_DW_OVERWRITE): sum_t dy xh,
- *   sum_t dy; db may be NULL; dx, dw and db share no memory
+ *   sum_t dy; db may be NULL; dx, dw and db share no memory, nor dx with what
+ *   the rows come from (but dx may be an fp32 x)
  * The sums over the rows run in a fixed order: the results are the same on
  * every run.  ws: omni_layer_norm_bwd_workspace_size(L, d) bytes, 256-byte
  * aligned.  Limits as for the forward; fp32 arrays 16-byte aligned (mean,
@@ -440,7 +442,8 @@ int omni_layer_norm_bwd(const void *x, const float *mean, const float *rstd, con
  * unpack (scale bytes up to 254): y [L, d] bf16 = value, or value * w + b rounded once (w, b [d] bf16;
  *         b may be NULL, and w with it): the normed tokens from
  *         omni_layer_norm_fwd's checkpoint
- * d % 32 == 0.  x, q, y, w, b 16-byte aligned.
+ * d % 32 == 0.  x, q, y, w, b 16-byte aligned; the output shares no memory with
+ * the rows it is made from.
  */
 int omni_act_pack(const void *x, int L, int d, uint8_t *q, uint8_t *scale, unsigned flags,
                   omni_stream_t stream);

@@ -795,6 +795,23 @@ def test_bindings_give_what_the_wrappers_give():
             assert (t - base - g[k]).norm() <= 1e-5 * (g[k].norm() + base * g[k].numel() ** 0.5), k
 
 
+@pytest.mark.parametrize("L,d", [(3, 8), (1000, 8), (700, 776), (5000, 1024), (300, 8192)])
+def test_rows_written_in_place(L, d):
+    """y over a bf16 x, dx over an fp32 x: bit for bit what separate arrays give."""
+    x, w, b, dy = _rows(L, d, torch.bfloat16, L)
+    want = omni.layer_norm_fwd(x, w, b)
+    omni.omni_layer_norm_fwd(x, w, b, L, d, 1e-5, x, None, None, None, None, 0)
+    assert torch.equal(x, want["y"])
+    x = _rows(L, d, torch.float32, L + 1)[0]
+    f = omni.layer_norm_fwd(x, w, b)
+    kept = dict(mean=f["mean"])
+    want = omni.layer_norm_bwd(dy, w, f["rstd"], x=x, **kept)
+    base = x.clone()
+    got = omni.layer_norm_bwd(dy, w, f["rstd"], x=x, **kept, dx=x)
+    assert torch.equal(x, base + want["dx"]) and got["dx"] is x
+    assert torch.equal(got["dw"], want["dw"]) and torch.equal(got["db"], want["db"])
+
+
 def test_overwrite_does_not_read_the_gradients():
     """OMNI_DW_OVERWRITE on buffers full of NaN, through the C entry points."""
     L, d, N_r, N_c, K = 70, 256, 20, 30, 4

@@ -270,6 +270,41 @@ def test_wrappers_refuse_sizes_past_31_bits(lib, n):
             call()
 
 
+@pytest.mark.parametrize("shift", [0, 16, -16, "end"])
+def test_outputs_over_rows_still_to_be_read_are_refused(lib, shift):
+    """Other threads would write over rows that a thread has yet to read.  Only a
+    row written in place, byte for byte where it was read, is sound."""
+    L, d, N = 4, 64, 96
+    x = 16 << 24
+
+    def over(args, at, n_in, n_out):
+        bad = list(args)
+        bad[at] = _p(x + (n_in - 16 if shift == "end" else shift if shift >= 0 else 16 - n_out))
+        return bad
+
+    fwd = [_p(x), FAKE, None, L, d, 1e-5, APART[0], None, None, None, None, 0, None]
+    if shift != 0:                                       # y over x itself, both bf16, is in place
+        assert lib.omni_layer_norm_fwd(*over(fwd, 6, 2 * L * d, 2 * L * d)) == -1
+    fwd[11] = omni.OMNI_X_F32
+    assert lib.omni_layer_norm_fwd(*over(fwd, 6, 4 * L * d, 2 * L * d)) == -1
+    fwd[9], fwd[10] = APART[1], APART[2]
+    assert lib.omni_layer_norm_fwd(*over(fwd, 9, 4 * L * d, L * d)) == -1
+    bwd = [_p(x), FAKE, FAKE, None, None, FAKE, _p(9 << 24), L, d, *APART[:3], 0, FAKE, BIG, None]
+    assert lib.omni_layer_norm_bwd(*over(bwd, 9, 2 * L * d, 4 * L * d)) == -1
+    if shift != 0:                                       # dx over x itself, both fp32, is in place
+        bwd[12] = omni.OMNI_X_F32
+        assert lib.omni_layer_norm_bwd(*over(bwd, 9, 4 * L * d, 4 * L * d)) == -1
+    bwd[0], bwd[3], bwd[4], bwd[12] = None, _p(x), FAKE, 0
+    assert lib.omni_layer_norm_bwd(*over(bwd, 9, L * d, 4 * L * d)) == -1
+    for flags, size in ((0, 2), (omni.OMNI_X_F32, 4)):
+        pack = [_p(x), L, d, APART[0], FAKE, flags, None]
+        assert lib.omni_act_pack(*over(pack, 3, size * L * d, L * d)) == -1
+    unpack = [_p(x), FAKE, None, None, L, d, APART[0], None]
+    assert lib.omni_act_unpack(*over(unpack, 6, L * d, 2 * L * d)) == -1
+    counts = [_p(x), None, L, 16, N, APART[0], APART[1], FAKE, 256, None]
+    assert lib.omni_expert_counts(*over(counts, 5, 4 * L * 16, 4 * N)) == -1
+
+
 def test_layer_fwd_refuses_half_a_norm(lib):
     x, w = torch.zeros(4, 256, dtype=torch.bfloat16), torch.ones(256, dtype=torch.bfloat16)
     for given in (dict(norm_b=w), dict(norm_eps=1e-6), dict(norm_b=w, norm_eps=0.0)):
