@@ -100,9 +100,10 @@ __device__ __forceinline__ int exp_of(uint32_t bits) {
 }
 // Exponent by which a token's ds is scaled, from its loss: P U and P l are at
 // most l, since all terms of l = sum P U are positive and P <= 1, so no |P (U - l)|
-// is above it, and the largest is near it where the token's losses lie on few
-// experts.  Below 2^-60 some P is under 2^-30 and has lost its last bits already;
-// above 2^40 is no finite l of counts below 2^31.
+// is above it, and the largest is near it where the token's loss lies on few
+// experts.  (P may be up to 3.99 where it is not normalised: ds then stays below
+// 2^16 x 0.998, which fp16 holds.)  Below 2^-60 some P is under 2^-30 and has lost
+// its last bits already; counts below 2^31 give no finite l above 2^40.
 __device__ __forceinline__ int token_exp(float l) {
     const int e = exp_of(__float_as_uint(l) & 0x7fffffffu);
     return e < -60 ? -60 : e > 40 ? 40 : e;
