@@ -35,12 +35,12 @@
 // themselves, and by 4e-3 for a collapsed router, where U - l_t cancels.  A
 // scale of ds by the largest count left 6e-5 at 1304 x 1304 and 1e-2 at 8192 x
 // 8192 where spread probabilities meet tasks on one expert.  With these, and
-// with what kChunk below says, the gradients' errors against 64 bits are near
-// those of torch in fp32, a little above or below by the inputs: headline
-// 5.6e-7 and 1.2e-6, skewed layer 1.3e-6 to 2.3e-6 and 2.0e-6 to 2.7e-6 (four
-// seeds).  They are up to twice torch's where U and l agree in all but their
-// last bits (counts of millions on every expert: 3.5e-5 and 1.7e-5), since both
-// are cut off towards zero, by different amounts.
+// with what kChunk below says, the gradients' errors against 64 bits are 0.4 to
+// 1.6 times those of torch in fp32: headline 5.6e-7 and 1.2e-6, skewed layer
+// 1.3e-6 to 2.3e-6 and 1.8e-6 to 2.7e-6 (five seeds).  The losses' are up to 2.6
+// times (8e-8 and 3e-8), and the gradients' twice torch's where U and l agree in
+// all but their last bits (counts of millions on every expert: 3.5e-5 and
+// 1.7e-5), since both are cut off towards zero, by different amounts.
 //
 // Bounds and measurements, headline layer (L = 4096, d = 1024, 1304 x 1304
 // grid, one B200, clocks under load): the products are 28 GFLOP forward, 56 +
@@ -511,7 +511,7 @@ constexpr int kMaxProbs = 2, kMaxMaps = 6;
 // small, then the 8 of the hi halves; the additions in registers round to
 // nearest.  Headline step, and largest error against 64 bits there and at the
 // skewed layer: 2 steps 266 us, 5e-7, 1.3e-6; 4 steps 248 us, 7e-7, 2.9e-6; 8
-// steps, halves together, 227 us, 2e-6, 5.6e-6 (torch in fp32: 1.2e-6, 2.0e-6
+// steps, halves together, 227 us, 2e-6, 5.6e-6 (torch in fp32: 1.2e-6, 1.8e-6
 // to 2.7e-6 by the seed).
 // A backward tile's first two accumulators take up to kMaxLead steps (a fifth
 // of them at most): they are computed while the warps that would drain them
